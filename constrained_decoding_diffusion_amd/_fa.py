@@ -20,15 +20,20 @@ FA_DFA, FA_NFA, FA_LABEL_RANGES, FA_NO_TRIM = 1, 2, 4, 8
 FA_FIRST_LEVEL_SPARSE, FA_FIRST_LEVEL_DENSE, FA_SECOND_LEVEL_SPARSE = 16, 32, 64
 FA_LIVE_STATES = 128
 FA_FIRST_LEVEL_PAIRS = 256
+FA_BEAMS = 512
 FA_CONF_PROB, FA_CONF_NEGENT, FA_CONF_UNCONSTRAINED = 0, 1, 2
 FA_PROF_NONE, FA_PROF_EMISSION_DENSE, FA_PROF_TREE_LEVEL1, FA_PROF_MARG_Q = range(4)
 FA_PROBE_READ, FA_PROBE_COPY = 0, 1
+FA_F32, FA_F16, FA_BF16 = 0, 1, 2
+FA_BEAM_LOGITS, FA_BEAM_PROBS = 0, 1
+FA_BEAM_MAX = 64
 
 EXPORTS = ["fa_compile_table", "fa_table_upload", "fa_table_destroy", "fa_table_info",
            "fa_table_state_map", "fa_sizes", "fa_build_transitions", "fa_span_tree", "fa_sample",
            "fa_marginals", "fa_sample_marginals", "fa_commit", "fa_strerror", "fa_profile_kernel",
            "fa_span_tree_noalloc", "fa_probe_bandwidth", "fa_map_sizes", "fa_map_decode",
-           "fa_chain_sample", "fa_chain_sample_marginals"]
+           "fa_chain_sample", "fa_chain_sample_marginals", "fa_beam_sizes", "fa_beam_lookahead",
+           "fa_beam_start", "fa_beam_select", "fa_beam_reorder", "fa_beam_trace"]
 FA_SPAN_TREE_NOALLOC_MAX_BYTES = 8 << 20
 
 
@@ -36,6 +41,13 @@ class FaError(RuntimeError):
     def __init__(self, fn: str, code: int):
         super().__init__(f"{fn}: {lib().fa_strerror(code).decode()} (code {code})")
         self.code = code
+
+
+class _BeamItem(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p)] + [
+        (f, C.c_int64) for f in ("src_batch_stride", "src_beam_stride", "src_row_stride",
+                                 "dst_batch_stride", "dst_beam_stride", "dst_row_stride", "rows",
+                                 "row_bytes")]
 
 
 _lib = None
@@ -74,6 +86,13 @@ def lib():
     L.fa_chain_sample.argtypes = [P, P, I32, I32, P, U64, P, P, P, P, SZ, P, P]
     L.fa_chain_sample_marginals.argtypes = [P, P, I32, I32, P, U64, I32, P, P, P, P, P, P, SZ, P, P]
     L.fa_map_decode.argtypes = [P, P, I32, I32, P, P, SZ, P, P, P, P, P]
+    L.fa_beam_sizes.argtypes = [P, I32, I32, P, P]
+    L.fa_beam_lookahead.argtypes = [P, I32, P, P]
+    L.fa_beam_start.argtypes = [P, I32, I32, P, P, P]
+    L.fa_beam_select.argtypes = [P, I32, P, I64, I64, I32, I32, I32, I32, P, P, P, I32, P, P, P, P,
+                                 P, SZ, P, P]
+    L.fa_beam_reorder.argtypes = [P, I32, I32, I32, P, P]
+    L.fa_beam_trace.argtypes = [I32, I32, I32, P, P, P, P]
     L.fa_strerror.argtypes = [C.c_int]
     L.fa_strerror.restype = C.c_char_p
     for fn in EXPORTS:
@@ -95,7 +114,7 @@ def _np_ptr(a: np.ndarray):
 INFO_KEYS = ["S", "Sp", "start", "n_accept", "pairs", "list_pairs", "dense_pairs", "range_pairs",
              "list_entries", "segments", "cuts", "sel_tokens", "use_sel", "V", "S_orig",
              "first_sparse", "first_work", "second_sparse", "second_work", "pairs2", "leafless",
-             "leaf_msg_pairs", "live_states", "first_pairs", "map_first_sparse"]
+             "leaf_msg_pairs", "live_states", "first_pairs", "map_first_sparse", "beams"]
 
 
 class Table:
@@ -124,18 +143,21 @@ class Table:
         self.orig = orig
 
     @classmethod
-    def from_automaton(cls, aut, flags=None, first_level="auto", live_states=False):
+    def from_automaton(cls, aut, flags=None, first_level="auto", live_states=False, beams=False):
         """first_level: "auto" (the library's choice), "sparse" (first span
         level from the pair values), "sparse2" (also the second level, from
         the two-step pattern), "dense" (dense matrix products over dense
         leaves) or "pairs" (dense matrix products whose operands are staged
         from the pair values; no dense leaves).
         live_states: FA_LIVE_STATES (span products over the states live at
-        their midpoint under each step's p)."""
+        their midpoint under each step's p).
+        beams: FA_BEAMS (the image also serves beam_select)."""
         if flags is None:
             flags = (FA_DFA if aut.dfa else FA_NFA) | (FA_LABEL_RANGES if aut.ranges else 0)
         if live_states:
             flags |= FA_LIVE_STATES
+        if beams:
+            flags |= FA_BEAMS
         flags |= {"auto": 0, "sparse": FA_FIRST_LEVEL_SPARSE,
                   "dense": FA_FIRST_LEVEL_DENSE, "pairs": FA_FIRST_LEVEL_PAIRS,
                   "sparse2": FA_FIRST_LEVEL_SPARSE | FA_SECOND_LEVEL_SPARSE}[first_level]
@@ -340,6 +362,266 @@ def map_decode(table: Table, p, bufs: "MapBuffers" = None):
         _ptr(bufs.logmax), _ptr(bufs.states), _ptr(bufs.tokens), _ptr(bufs.status),
         C.c_void_p(stream)))
     return bufs
+
+
+class BeamBuffers:
+    """K hypotheses per batch row: scores [B, K] (fp32 cumulative
+    log-probabilities, -inf an empty slot), states [B, K, words] (int32
+    bitsets over the table's compact states), the tokens and parents [B, K] of
+    the step that made them, the rows' status [B], and beam_select's
+    workspace.  ``like``: take status and workspace from another BeamBuffers
+    of the same search."""
+
+    def __init__(self, table: Table, B: int, K: int, device="cuda", like: "BeamBuffers" = None):
+        import torch
+        n, w = C.c_size_t(), C.c_int32()
+        _check("fa_beam_sizes", lib().fa_beam_sizes(table.handle, B, K, C.byref(n), C.byref(w)))
+        self.B, self.K, self.words = B, K, w.value
+        if like is not None:
+            device = like.scores.device
+        self.scores = torch.empty((B, K), dtype=torch.float32, device=device)
+        self.states = torch.empty((B, K, w.value), dtype=torch.int32, device=device)
+        self.tokens = torch.empty((B, K), dtype=torch.int32, device=device)
+        self.parents = torch.empty((B, K), dtype=torch.int32, device=device)
+        self.status = torch.zeros(B, dtype=torch.int32, device=device) if like is None else like.status
+        if like is not None and like.ws.numel() >= n.value:
+            self.ws = like.ws
+        else:
+            self.ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _device_of(table: Table, t):
+    """Uploads the table where t lives if it is nowhere yet."""
+    if table.buf is None:
+        table.upload(t.device)
+    elif table.buf.device != t.device:
+        raise ValueError(f"the table is on {table.buf.device}, the input on {t.device}")
+    return t.device
+
+
+def _on(device):
+    """The device made current (HIP launches go to the current device), and
+    torch's current stream of it."""
+    import torch
+    return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+
+
+def beam_lookahead(table: Table, L: int, device="cuda"):
+    """fa_beam_lookahead: int32 [L + 1, words], row r the bitset of the states
+    from which the automaton accepts after exactly r more tokens.  It depends
+    on the table and L only."""
+    import torch
+    if table.buf is None:
+        table.upload(device)
+    sets = torch.empty((max(L, 0) + 1, (table.info["S"] + 31) // 32), dtype=torch.int32,
+                       device=table.buf.device)
+    guard, stream = _on(sets.device)
+    with guard:
+        _check("fa_beam_lookahead", lib().fa_beam_lookahead(table.handle, L, _ptr(sets),
+                                                            C.c_void_p(stream)))
+    return sets
+
+
+def beam_start(table: Table, B: int, K: int, device="cuda"):
+    """Hypotheses before the first step (fa_beam_start): slot 0 of every row
+    the empty string, the other slots empty; no row flagged."""
+    if table.buf is None:
+        table.upload(device)
+    beams = BeamBuffers(table, B, K, device=table.buf.device)
+    guard, stream = _on(table.buf.device)
+    with guard:
+        _check("fa_beam_start", lib().fa_beam_start(table.handle, B, K, _ptr(beams.scores),
+                                                    _ptr(beams.states), C.c_void_p(stream)))
+    return beams
+
+
+def _beam_dtype(t):
+    import torch
+    code = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"logits must be float32, float16 or bfloat16, not {t.dtype}")
+    return code
+
+
+def beam_select(table: Table, logits, beams: BeamBuffers, out: BeamBuffers = None,
+                mode: int = FA_BEAM_LOGITS, steps_left: int = 0, lookahead=None):
+    """One step of a beam search (fa_beam_select) on torch's current stream:
+    the out.K best of beams.K x V candidates of every row under the table's
+    automaton.  logits: cuda [B, beams.K, V] float32, float16 or bfloat16,
+    contiguous in V (any other strides; a row expanded over the beams is read
+    as one); with FA_BEAM_PROBS the probabilities themselves.  lookahead:
+    beam_lookahead(table, L), with steps_left in 1..L the tokens still to
+    come, this one included; without one a hypothesis may run into a dead end.
+    Returns out (a new BeamBuffers of beams.K slots by default; not beams
+    itself), whose status is that of beams."""
+    if logits.dim() != 3 or tuple(logits.shape) != (beams.B, beams.K, table.info["V"]):
+        raise ValueError(f"logits has shape {tuple(logits.shape)}, expected "
+                         f"{(beams.B, beams.K, table.info['V'])}")
+    dtype = _beam_dtype(logits)
+    B, Kin, V = logits.shape
+    sb, sk, sv = logits.stride()
+    if not logits.is_cuda or (V > 1 and sv != 1):
+        raise ValueError("logits must be a cuda tensor, contiguous in its last dimension")
+    dev = _device_of(table, logits)
+    if out is None:
+        out = BeamBuffers(table, B, Kin, like=beams)
+    elif out is beams or out.B != B or out.words != beams.words:
+        raise ValueError("out must be other buffers of the same batch and table")
+    for t in (beams.scores, out.scores) + (() if lookahead is None else (lookahead,)):
+        if t.device != dev:
+            raise ValueError(f"the beams and the lookahead must be on {dev}")
+    if lookahead is None:
+        if steps_left != 0:
+            raise ValueError("steps_left needs a lookahead")
+    elif (lookahead.dim() != 2 or lookahead.shape[1] != beams.words or not lookahead.is_contiguous()
+          or lookahead.element_size() != 4):
+        raise ValueError("lookahead must come from beam_lookahead of this table")
+    elif not 1 <= steps_left < lookahead.shape[0]:
+        raise ValueError(f"steps_left is {steps_left}, the lookahead covers 1..{lookahead.shape[0] - 1}")
+    guard, stream = _on(dev)
+    with guard:
+        _check("fa_beam_select", lib().fa_beam_select(
+            table.handle, dtype, _ptr(logits), sb if B > 1 else 0, sk if Kin > 1 else 0, B, Kin,
+            out.K, mode, _ptr(beams.scores), _ptr(beams.states), _ptr(lookahead), steps_left,
+            _ptr(out.scores), _ptr(out.tokens), _ptr(out.parents), _ptr(out.states),
+            _ptr(beams.ws), beams.ws.numel(), _ptr(beams.status), C.c_void_p(stream)))
+    out.status = beams.status
+    return out
+
+
+def _slot_rows(t):
+    """(rows, row stride, row bytes) of a slot of t [B, K, ...]: its inner
+    dimensions as equal pieces at equal distances."""
+    e = t.element_size()
+    dims = [(n, s * e) for n, s in zip(t.shape[2:], t.stride()[2:]) if n != 1]
+    if any(n == 0 for n, _ in dims):
+        return 0, 0, 0
+    row = e
+    while dims and dims[-1][1] == row:
+        row *= dims.pop()[0]
+    if not dims:
+        return 1, row, row
+    n, stride = dims.pop()
+    while dims and dims[-1][1] == n * stride:
+        n *= dims.pop()[0]
+    if dims:
+        raise ValueError("a slot must be equal contiguous pieces at equal distances "
+                         f"(shape {tuple(t.shape)}, strides {t.stride()})")
+    return n, stride, row
+
+
+def beam_reorder(tensors, parents, out=None):
+    """Moves per-hypothesis memory after the chosen parents
+    (fa_beam_reorder) on torch's current stream: slot (b, k) of every tensor
+    becomes its slot (b, parents[b, k]).  tensors: cuda [B, K, ...] of any
+    types, views included (the valid part of longer caches), each slot one
+    contiguous piece or equal pieces at equal distances.  In place, or into
+    ``out`` (tensors of the same shapes and types that share no memory with
+    the sources).  parents: cuda int32 [B, K].  Returns out, or tensors."""
+    import torch
+    if parents.dim() != 2 or parents.dtype != torch.int32 or not parents.is_contiguous() \
+            or not parents.is_cuda:
+        raise ValueError("parents must be a contiguous cuda int32 [B, K] tensor")
+    B, K = parents.shape
+    dst = tensors if out is None else out
+    if len(dst) != len(tensors):
+        raise ValueError("out must hold one tensor for each of tensors")
+    items = (_BeamItem * max(len(tensors), 1))()
+    for it, s, d in zip(items, tensors, dst):
+        if s.dim() < 2 or tuple(s.shape[:2]) != (B, K) or s.shape != d.shape or s.dtype != d.dtype:
+            raise ValueError(f"expected [{B}, {K}, ...] tensors, and out of the same shapes and types")
+        if s.device != parents.device or d.device != parents.device:
+            raise ValueError(f"every tensor must be on {parents.device}")
+        rows, sr, row = _slot_rows(s)
+        rows_d, dr, row_d = (rows, sr, row) if d is s else _slot_rows(d)
+        # the common pieces of both layouts
+        piece = min(row, row_d)
+        if (rows, row) != (rows_d, row_d):
+            if piece == 0 or row % piece or row_d % piece:
+                raise ValueError("tensors and out cut their slots into different pieces")
+            if rows == 1:
+                rows, sr, row = row // piece, piece, piece
+            if rows_d == 1:
+                rows_d, dr, row_d = row_d // piece, piece, piece
+            if (rows, row) != (rows_d, row_d):
+                raise ValueError("tensors and out cut their slots into different pieces")
+        e = s.element_size()
+        it.src, it.dst = s.data_ptr(), d.data_ptr()
+        it.src_batch_stride, it.src_beam_stride, it.src_row_stride = s.stride(0) * e, s.stride(1) * e, sr
+        it.dst_batch_stride, it.dst_beam_stride, it.dst_row_stride = d.stride(0) * e, d.stride(1) * e, dr
+        it.rows, it.row_bytes = rows, row
+    guard, stream = _on(parents.device)
+    with guard:
+        _check("fa_beam_reorder", lib().fa_beam_reorder(items, len(tensors), B, K, _ptr(parents),
+                                                        C.c_void_p(stream)))
+    return dst
+
+
+def beam_trace(tokens, parents):
+    """The hypotheses of T recorded steps (fa_beam_trace) on torch's current
+    stream: tokens, parents cuda int32 [T, B, K] as beam_select left them;
+    returns int32 [B, K, T]."""
+    import torch
+    for t in (tokens, parents):
+        if t.dim() != 3 or t.dtype != torch.int32 or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError("tokens and parents must be contiguous cuda int32 [T, B, K] tensors")
+    if tokens.shape != parents.shape or tokens.device != parents.device:
+        raise ValueError("tokens and parents must have one shape and device")
+    T, B, K = tokens.shape
+    res = torch.empty((B, K, T), dtype=torch.int32, device=tokens.device)
+    guard, stream = _on(tokens.device)
+    with guard:
+        _check("fa_beam_trace", lib().fa_beam_trace(T, B, K, _ptr(tokens), _ptr(parents), _ptr(res),
+                                                    C.c_void_p(stream)))
+    return res
+
+
+def beam_search(table: Table, model, B: int, L: int, K: int, caches=(), mode: int = FA_BEAM_LOGITS,
+                device="cuda"):
+    """Left-to-right decoding of L tokens with K hypotheses per row under the
+    table's automaton: every hypothesis kept can still end in an accepting
+    state, and after L steps does.  model(t, tokens) gives the logits
+    [B, K, V] of position t (as beam_select takes them), tokens [B, K] being
+    those chosen at t - 1 (None at 0); ``caches`` ([B, K, ...] tensors, the
+    model's memory of each hypothesis) are reordered in place after every
+    step.  Returns (tokens int32 [B, K, L], beams): the hypotheses in
+    descending order of beams.scores, -1 in empty slots and in rows
+    beams.status flags."""
+    import torch
+    if L < 1:
+        raise ValueError("L must be at least 1")
+    beams = beam_start(table, B, K, device=device)
+    spare = BeamBuffers(table, B, K, like=beams)
+    ahead = beam_lookahead(table, L)
+    dev = beams.scores.device
+    tokens = torch.empty((L, B, K), dtype=torch.int32, device=dev)
+    parents = torch.empty((L, B, K), dtype=torch.int32, device=dev)
+    for t in range(L):
+        logits = model(t, tokens[t - 1] if t else None)
+        spare.tokens, spare.parents = tokens[t], parents[t]
+        beams, spare = beam_select(table, logits, beams, out=spare, mode=mode, steps_left=L - t,
+                                   lookahead=ahead), beams
+        if len(caches):
+            beam_reorder(caches, beams.parents)
+    hyp = beam_trace(tokens, parents)
+    return hyp.masked_fill_((beams.scores == float("-inf"))[..., None], -1), beams
+
+
+def beam_decode(table: Table, p, K: int):
+    """K likely accepted strings of one denoising step: a beam search over the
+    positions of p (cuda float32 [B, L, V], the p of step() and
+    map_decode()).  The best K found, which are not always the K best;
+    map_decode() gives the single best for certain.  Returns what
+    beam_search() returns, the scores being ln of the strings'
+    probabilities."""
+    import torch
+    if p.dim() != 3 or p.shape[2] != table.info["V"]:
+        raise ValueError(f"p has shape {tuple(p.shape)}, expected [B, L, {table.info['V']}]")
+    if not p.is_cuda or p.dtype != torch.float32 or not p.is_contiguous():
+        raise ValueError("p must be a contiguous cuda float32 tensor")
+    B, L, V = p.shape
+    return beam_search(table, lambda t, tokens: p[:, t, None].expand(B, K, V), B, L, K,
+                       mode=FA_BEAM_PROBS, device=p.device)
 
 
 def probe_bandwidth(mode: int, src, dst, nbytes: int, blocks: int, stream):

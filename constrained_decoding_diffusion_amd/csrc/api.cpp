@@ -376,6 +376,129 @@ extern "C" int fa_commit(int32_t B, int32_t L, int32_t V, const float *conf,
                                 stream));
 }
 
+namespace {
+
+// rows and granules the selection takes; FA_OK or the refusal
+int beam_size_check(const fa_table *t, int32_t B, int32_t Kin)
+{
+    if (!t || B < 0 || Kin < 1 || Kin > FA_BEAM_MAX) return FA_EINVAL;
+    if ((int64_t)Kin * beam_grans(t->h.V) > kBeamGranMax) return FA_ETOOBIG;
+    return FA_OK;
+}
+
+int32_t set_words(const fa_table *t) { return (t->h.S + 31) / 32; }
+
+}  // namespace
+
+extern "C" int fa_beam_sizes(const fa_table *t, int32_t B, int32_t Kin, size_t *ws_bytes,
+                             int32_t *words)
+{
+    if (int rc = beam_size_check(t, B, Kin)) return rc;
+    if (ws_bytes) *ws_bytes = std::max<size_t>(beam_ws_layout(t->h, B, Kin).total, 256);
+    if (words) *words = set_words(t);
+    return FA_OK;
+}
+
+extern "C" int fa_beam_lookahead(const fa_table *t, int32_t L, uint32_t *sets, fa_stream_t stream)
+{
+    if (!t || L < 0 || !sets) return FA_EINVAL;
+    if (L >= (1 << 24) || t->h.S > kBeamStatesMax) return FA_ETOOBIG;
+    if (int rc = ready(t)) return rc;
+    return hip_rc(launch_beam_lookahead(t->h.device_view(), L, sets, stream));
+}
+
+extern "C" int fa_beam_start(const fa_table *t, int32_t B, int32_t K, float *scores,
+                             uint32_t *states, fa_stream_t stream)
+{
+    if (!t || B < 0 || K < 1 || K > FA_BEAM_MAX) return FA_EINVAL;
+    if (B > 0 && (!scores || !states)) return FA_EINVAL;
+    if (int rc = ready(t)) return rc;
+    if (B == 0) return FA_OK;
+    return hip_rc(launch_beam_start(t->h.device_view(), B, K, scores, states, stream));
+}
+
+extern "C" int fa_beam_select(const fa_table *t, int32_t dtype, const void *logits,
+                              int64_t batch_stride, int64_t beam_stride, int32_t B, int32_t Kin,
+                              int32_t K, int32_t mode, const float *scores_in,
+                              const uint32_t *states_in, const uint32_t *lookahead,
+                              int32_t steps_left, float *scores, int32_t *tokens,
+                              int32_t *parents, uint32_t *states, void *ws, size_t ws_bytes,
+                              int32_t *row_status, fa_stream_t stream)
+{
+    if (int rc = beam_size_check(t, B, Kin)) return rc;
+    if (!t->h.beams) return FA_EINVAL;
+    if (K < 1 || K > FA_BEAM_MAX) return FA_EINVAL;
+    if (dtype < FA_F32 || dtype > FA_BF16 || mode < FA_BEAM_LOGITS || mode > FA_BEAM_PROBS)
+        return FA_EINVAL;
+    if (batch_stride < 0 || beam_stride < 0) return FA_EINVAL;
+    if (lookahead ? steps_left < 1 : steps_left != 0) return FA_EINVAL;
+    if (B == 0) return ready(t);
+    if (!logits || !scores_in || !states_in || !scores || !tokens || !parents || !states || !ws ||
+        !row_status)
+        return FA_EINVAL;
+    if (scores == scores_in || states == states_in) return FA_EINVAL;
+    if (((uintptr_t)logits & (dtype == FA_F32 ? 3 : 1)) || ((uintptr_t)ws & 15)) return FA_EINVAL;
+    const BeamWs w = beam_ws_layout(t->h, B, Kin);
+    if (ws_bytes < w.total) return FA_EINVAL;
+    if (int rc = ready(t)) return rc;
+    BeamSelect a;
+    a.logits = logits;
+    a.batch_stride = batch_stride;
+    a.beam_stride = beam_stride;
+    a.B = B;
+    a.Kin = Kin;
+    a.K = K;
+    a.mode = mode;
+    a.dtype = dtype;
+    a.scores_in = scores_in;
+    a.states_in = states_in;
+    a.reach = lookahead ? lookahead + (size_t)(steps_left - 1) * set_words(t) : nullptr;
+    a.scores = scores;
+    a.tokens = tokens;
+    a.parents = parents;
+    a.states = states;
+    a.status = row_status;
+    const int e = launch_beam_select(t->h.device_view(), a, (uint8_t *)ws, w, stream);
+    return e < 0 ? FA_ETOOBIG : hip_rc(e);
+}
+
+extern "C" int fa_beam_reorder(const fa_beam_item *items, int32_t n_items, int32_t B, int32_t K,
+                               const int32_t *parents, fa_stream_t stream)
+{
+    if (n_items < 0 || B < 0 || K < 1 || K > FA_BEAM_MAX) return FA_EINVAL;
+    if (n_items == 0 || B == 0) return FA_OK;
+    if (!items || !parents) return FA_EINVAL;
+    for (int32_t i = 0; i < n_items; ++i) {
+        const fa_beam_item &x = items[i];
+        if (x.rows < 0 || x.row_bytes < 0) return FA_EINVAL;
+        if (x.rows == 0 || x.row_bytes == 0) continue;
+        if (!x.src || !x.dst) return FA_EINVAL;
+        if (x.src_batch_stride < 0 || x.src_beam_stride < 0 || x.src_row_stride < 0 ||
+            x.dst_batch_stride < 0 || x.dst_beam_stride < 0 || x.dst_row_stride < 0)
+            return FA_EINVAL;
+        if (x.src == x.dst &&
+            (x.src_batch_stride != x.dst_batch_stride || x.src_beam_stride != x.dst_beam_stride ||
+             x.src_row_stride != x.dst_row_stride))
+            return FA_EINVAL;
+        // the slots of one dst must not share memory
+        if ((B > 1 && x.dst_batch_stride == 0) || (K > 1 && x.dst_beam_stride == 0) ||
+            (x.rows > 1 && x.dst_row_stride < x.row_bytes))
+            return FA_EINVAL;
+    }
+    const int e = launch_beam_reorder(items, n_items, B, K, parents, stream);
+    return e < 0 ? FA_ETOOBIG : hip_rc(e);
+}
+
+extern "C" int fa_beam_trace(int32_t T, int32_t B, int32_t K, const int32_t *tokens,
+                             const int32_t *parents, int32_t *out, fa_stream_t stream)
+{
+    if (T < 0 || B < 0 || K < 1 || K > FA_BEAM_MAX) return FA_EINVAL;
+    if (T >= (1 << 24)) return FA_ETOOBIG;
+    if (T == 0 || B == 0) return FA_OK;
+    if (!tokens || !parents || !out) return FA_EINVAL;
+    return hip_rc(launch_beam_trace(T, B, K, tokens, parents, out, stream));
+}
+
 extern "C" const char *fa_strerror(int code)
 {
     switch (code) {

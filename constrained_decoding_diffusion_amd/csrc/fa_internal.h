@@ -63,6 +63,13 @@ constexpr size_t map_range_lds(int ncut)
     return ((size_t)nint + (size_t)nblk * map_range_levels(nblk)) * sizeof(uint32_t);
 }
 
+// beam search: the vocabulary is cut into granules of this many tokens; a
+// wavefront's lane holds eight of them
+constexpr int kBeamGran = 512;
+constexpr int kBeamGranMax = 32768;   // granules of a row's hypotheses the selection holds in registers
+constexpr int kBeamStatesMax = 1 << 18;  // states whose two bitsets fit the lookahead's LDS
+constexpr int beam_grans(int V) { return (V + kBeamGran - 1) / kBeamGran; }
+
 enum PairClass : int32_t { kList = 0, kDense = 1, kRange = 2 };
 
 // The message pass's leaf level runs from the pair values (marg_leaf) when
@@ -159,6 +166,15 @@ struct DevTable {
     const int32_t *sel_lb;     // [V/256 + 2] first sel_tok index at or after token 256 t
     const int32_t *pair_colpos;  // [npairs] position of each pair in col_pairs
     int32_t n_tm;              // token-major LIST entries
+    // FA_BEAMS: the edges of every state, token-sorted.  LIST pairs as
+    // (token, target) entries with the first entry at or after every granule,
+    // DENSE pairs as (dense index, target), RANGE pairs as (lo, hi, target)
+    const int32_t *bm_off;     // [S][beam_grans(V) + 1]
+    const int32_t *bm_ent;     // pairs
+    const int32_t *bm_doff;    // [S+1]
+    const int32_t *bm_dense;   // pairs
+    const int32_t *bm_soff;    // [S+1]
+    const int32_t *bm_seg;     // (lo, hi, target, 0)
 };
 
 // Host representation of a compiled automaton and its device image.
@@ -184,6 +200,8 @@ struct HostTable {
     std::vector<uint32_t> cutbits;
     std::vector<int32_t> sel_lb;
     std::vector<int32_t> pair_colpos;
+    std::vector<int32_t> bm_off, bm_ent, bm_doff, bm_dense, bm_soff, bm_seg;
+    bool beams = false;         // FA_BEAMS
     bool has_cnt = false;
     bool use_sel = false;
     bool selbit = false;
@@ -369,6 +387,36 @@ constexpr int kCommitMaxL = 8192;  // positions per row the selection holds in L
 int launch_commit(int B, int L, int V, const float *conf, const int32_t *tokens, int steps_left,
                   int32_t *committed, int32_t *fresh, float *p, const int32_t *status,
                   void *stream);
+
+// Beam search (beam.hip, beam_state.hip).
+struct BeamSelect {
+    const void *logits;
+    int64_t batch_stride, beam_stride;
+    int32_t B, Kin, K, mode, dtype;
+    const float *scores_in;
+    const uint32_t *states_in;
+    const uint32_t *reach;  // the lookahead row a token's target must lie in, or null
+    float *scores;
+    int32_t *tokens, *parents;
+    uint32_t *states;
+    int32_t *status;
+};
+struct BeamWs {
+    size_t gmax = 0;   // [B*Kin][granules] fp32: largest allowed value of each granule
+    size_t part = 0;   // [B*Kin][granules] (maximum, sum of exp) of each wavefront's tokens
+    size_t total = 0;
+};
+BeamWs beam_ws_layout(const HostTable &t, int32_t B, int32_t Kin);
+int launch_beam_lookahead(const DevTable &d, int L, uint32_t *sets, void *stream);
+int launch_beam_start(const DevTable &d, int B, int K, float *scores, uint32_t *states,
+                      void *stream);
+// FA_ETOOBIG as a negative value when the grid does not fit
+int launch_beam_select(const DevTable &d, const BeamSelect &a, uint8_t *ws, const BeamWs &w,
+                       void *stream);
+int launch_beam_reorder(const fa_beam_item *items, int n, int B, int K, const int32_t *parents,
+                        void *stream);
+int launch_beam_trace(int T, int B, int K, const int32_t *tokens, const int32_t *parents,
+                      int32_t *out, void *stream);
 
 }  // namespace fa
 

@@ -97,6 +97,12 @@ void build_image(HostTable &t)
     append_section(t.image, t.offs, t.w2_t);
     append_section(t.image, t.offs, t.col_a);
     append_section(t.image, t.offs, t.p2_col_a);
+    append_section(t.image, t.offs, t.bm_off);
+    append_section(t.image, t.offs, t.bm_ent);
+    append_section(t.image, t.offs, t.bm_doff);
+    append_section(t.image, t.offs, t.bm_dense);
+    append_section(t.image, t.offs, t.bm_soff);
+    append_section(t.image, t.offs, t.bm_seg);
     t.image.resize((t.image.size() + 255) & ~size_t(255));
 }
 
@@ -147,6 +153,7 @@ DevTable HostTable::device_view() const
     nxt(d.p2_a); nxt(d.p2_b); nxt(d.p2_row_ptr); nxt(d.p2_col_ptr); nxt(d.p2_col_pairs);
     nxt(d.p2_colpos); nxt(d.w1_n); nxt(d.w1_t); nxt(d.w2_n); nxt(d.w2_t);
     nxt(d.col_a); nxt(d.p2_col_a);
+    nxt(d.bm_off); nxt(d.bm_ent); nxt(d.bm_doff); nxt(d.bm_dense); nxt(d.bm_soff); nxt(d.bm_seg);
     d.second_sparse = second_sparse ? 1 : 0;
     d.live_states = live_states ? 1 : 0;
     d.np2 = (int32_t)p2_a.size();
@@ -383,6 +390,54 @@ static void window_offsets(const HostTable &t, const std::vector<int32_t> &rp,
     }
 }
 
+// the token-sorted edges of every state (FA_BEAMS); false when the granule
+// offsets exceed 31 bits
+static bool build_beams(HostTable &t)
+{
+    const int32_t nG = beam_grans(t.V);
+    if ((int64_t)t.S * (nG + 1) > std::numeric_limits<int32_t>::max()) return false;
+    t.bm_off.assign((size_t)t.S * (nG + 1), 0);
+    t.bm_doff.assign(t.S + 1, 0);
+    t.bm_soff.assign(t.S + 1, 0);
+    std::vector<std::pair<int32_t, int32_t>> ent;
+    std::vector<std::pair<std::pair<int32_t, int32_t>, int32_t>> seg;
+    for (int32_t a = 0; a < t.S; ++a) {
+        ent.clear();
+        seg.clear();
+        for (int32_t q = t.row_ptr[a]; q < t.row_ptr[a + 1]; ++q) {
+            const int32_t b = t.pair_b[q];
+            if (t.pair_cls[q] == kDense) {
+                t.bm_dense.push_back(t.pair_aux[q]);
+                t.bm_dense.push_back(b);
+            }
+            for (int32_t k = t.list_off[q]; k < t.list_off[q + 1]; ++k) ent.emplace_back(t.list_tok[k], b);
+            for (int32_t k = t.seg_off[q]; k < t.seg_off[q + 1]; ++k)
+                seg.push_back({{t.seg_lo[k], t.seg_hi[k]}, b});
+        }
+        std::sort(ent.begin(), ent.end());
+        std::sort(seg.begin(), seg.end());
+        size_t e = 0;
+        const size_t base = t.bm_ent.size() / 2;
+        for (int32_t g = 0; g <= nG; ++g) {
+            while (e < ent.size() && ent[e].first < (int64_t)g * kBeamGran) ++e;
+            t.bm_off[(size_t)a * (nG + 1) + g] = (int32_t)(base + e);
+        }
+        for (auto &x : ent) {
+            t.bm_ent.push_back(x.first);
+            t.bm_ent.push_back(x.second);
+        }
+        for (auto &x : seg) {
+            t.bm_seg.push_back(x.first.first);
+            t.bm_seg.push_back(x.first.second);
+            t.bm_seg.push_back(x.second);
+            t.bm_seg.push_back(0);
+        }
+        t.bm_doff[a + 1] = (int32_t)(t.bm_dense.size() / 2);
+        t.bm_soff[a + 1] = (int32_t)(t.bm_seg.size() / 4);
+    }
+    return true;
+}
+
 static int compile(int32_t S, int32_t V, int32_t start, const int32_t *accept, int32_t n_accept,
                    int64_t E, const int32_t *src, const int32_t *dst, const int64_t *label_off,
                    const int32_t *label_tok, uint32_t flags, HostTable &t)
@@ -393,7 +448,7 @@ static int compile(int32_t S, int32_t V, int32_t start, const int32_t *accept, i
     if ((flags & FA_DFA) && (flags & FA_NFA)) return FA_EINVAL;
     if (flags & ~uint32_t(FA_DFA | FA_NFA | FA_LABEL_RANGES | FA_NO_TRIM | FA_FIRST_LEVEL_SPARSE |
                           FA_FIRST_LEVEL_DENSE | FA_SECOND_LEVEL_SPARSE | FA_LIVE_STATES |
-                          FA_FIRST_LEVEL_PAIRS))
+                          FA_FIRST_LEVEL_PAIRS | FA_BEAMS))
         return FA_EINVAL;
     {
         const uint32_t first = flags & (FA_FIRST_LEVEL_SPARSE | FA_FIRST_LEVEL_DENSE | FA_FIRST_LEVEL_PAIRS);
@@ -866,6 +921,8 @@ static int compile(int32_t S, int32_t V, int32_t start, const int32_t *accept, i
     // writes it)
     t.leafless = (t.first_sparse || t.first_pairs) && np > 0 && !t.map_n.empty() &&
                  leaf_level_from_pairs(np, t.S, t.Sp);
+    t.beams = (flags & FA_BEAMS) != 0;
+    if (t.beams && !build_beams(t)) return FA_ETOOBIG;
     build_image(t);
     return FA_OK;
 }
@@ -912,7 +969,7 @@ extern "C" int fa_table_info(const fa_table *t, int64_t *info, int32_t n)
     const HostTable &h = t->h;
     int32_t nl = 0, nd = 0, nr = 0;
     for (int32_t c : h.pair_cls) (c == kList ? nl : c == kDense ? nd : nr)++;
-    constexpr int32_t kInfo = 25;
+    constexpr int32_t kInfo = 26;
     int64_t v[kInfo] = {h.S, h.Sp, h.start, (int64_t)h.acc.size(), h.npairs(), nl, nd, nr,
                         (int64_t)h.list_tok.size(), h.nseg(), h.ncut(), h.nsel(),
                         h.use_sel ? 1 : 0, h.V, h.S_orig, h.first_sparse ? 1 : 0, h.first_work,
@@ -920,7 +977,7 @@ extern "C" int fa_table_info(const fa_table *t, int64_t *info, int32_t n)
                         h.leafless ? 1 : 0,
                         h.npairs() > 0 && leaf_level_from_pairs(h.npairs(), h.S, h.Sp) ? 1 : 0,
                         h.live_states ? 1 : 0, h.first_pairs ? 1 : 0,
-                        h.map_first_sparse ? 1 : 0};
+                        h.map_first_sparse ? 1 : 0, h.beams ? 1 : 0};
     for (int32_t k = 0; k < n && k < kInfo; ++k) info[k] = v[k];
     return FA_OK;
 }

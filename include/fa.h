@@ -86,8 +86,10 @@ enum {
     FA_SECOND_LEVEL_SPARSE = 64, /* also the second level from the two-step pattern (needs the
                                     first level sparse) */
     FA_LIVE_STATES = 128, /* span products over the states live at their midpoint (see fa_span_tree) */
-    FA_FIRST_LEVEL_PAIRS = 256 /* first span level as dense matrix products whose operands are
-                                  staged from the pair values (no dense leaves) */
+    FA_FIRST_LEVEL_PAIRS = 256, /* first span level as dense matrix products whose operands are
+                                   staged from the pair values (no dense leaves) */
+    FA_BEAMS = 512 /* the image also holds the token-sorted edges of every state that
+                      fa_beam_select reads */
 };
 
 enum { FA_CONF_PROB = 0, FA_CONF_NEGENT = 1, FA_CONF_UNCONSTRAINED = 2 };
@@ -120,7 +122,9 @@ enum { FA_CONF_PROB = 0, FA_CONF_NEGENT = 1, FA_CONF_UNCONSTRAINED = 2 };
  *                   the first is sparse and its own work is at most 1/256 of
  *                   S^3), and FA_LIVE_STATES (fa_span_tree restricts the
  *                   256x256-tile products to the states live at their
- *                   midpoint under the step's p)
+ *                   midpoint under the step's p), and FA_BEAMS (the image
+ *                   also holds what fa_beam_select reads; no other call is
+ *                   affected)
  *   out             receives the handle (free with fa_table_destroy)
  *   device_bytes    receives the size of the device image
  * Dead states (unreachable from s0 or unable to reach F) are removed unless
@@ -162,7 +166,8 @@ void fa_table_destroy(fa_table *t);
  * the first level is a dense product with operands staged from the pair
  * values, [24] 1 if fa_map_decode forms its first max-plus level from the
  * pairs (FA_FIRST_LEVEL_SPARSE forces it and FA_FIRST_LEVEL_DENSE keeps it
- * dense; else when 256 [16] <= S^3).  Returns FA_OK or FA_EINVAL.
+ * dense; else when 256 [16] <= S^3), [25] 1 if the table was compiled with
+ * FA_BEAMS.  Returns FA_OK or FA_EINVAL.
  */
 int fa_table_info(const fa_table *t, int64_t *info, int32_t n);
 
@@ -445,6 +450,132 @@ int fa_map_decode(const fa_table *t, const float *p, int32_t B, int32_t L, doubl
 int fa_commit(int32_t B, int32_t L, int32_t V, const float *conf, const int32_t *tokens,
               int32_t steps_left, int32_t *committed, int32_t *fresh, float *p,
               const int32_t *row_status, fa_stream_t stream);
+
+/*
+ * Beam search under the automaton: K hypotheses per batch row, each with its
+ * cumulative log-probability and the set of automaton states its tokens lead
+ * to.  One step is fa_beam_select on the model's logits for the next position;
+ * fa_beam_reorder moves the model's own per-hypothesis memory (caches) after
+ * the chosen parents, and fa_beam_trace reads the finished hypotheses back
+ * from the recorded steps.  With p of one denoising step in place of logits
+ * the same loop gives the K best strings the search finds, where
+ * fa_map_decode gives the single best one.
+ *
+ * State sets are bitsets over the table's compact states (fa_table_state_map
+ * gives their original ids): bit s % 32 of word s / 32, W = ceil(S' / 32)
+ * words.  On a DFA a live hypothesis has one bit set.
+ */
+enum { FA_F32 = 0, FA_F16 = 1, FA_BF16 = 2 };
+enum { FA_BEAM_LOGITS = 0, FA_BEAM_PROBS = 1 };
+#define FA_BEAM_MAX 64 /* hypotheses per row */
+
+/*
+ * fa_beam_sizes - workspace bytes of fa_beam_select with batch B and Kin
+ * hypotheses per row, and the words W of one state set.  Either output may be
+ * NULL.  Errors: FA_EINVAL (B < 0, Kin outside 1..FA_BEAM_MAX), FA_ETOOBIG
+ * (Kin ceil(V / 512) > 32768: 262,144 tokens at 64 hypotheses).
+ */
+int fa_beam_sizes(const fa_table *t, int32_t B, int32_t Kin, size_t *ws_bytes, int32_t *words);
+
+/*
+ * fa_beam_lookahead - the states from which the automaton can still accept:
+ * row r of `sets` (r = 0..L) is the bitset of the states from which some
+ * accepting state is exactly r tokens away.  It depends on the table and L
+ * only; fa_beam_select takes it to keep hypotheses out of dead ends.
+ *   sets  device uint32 [L+1][W]
+ * Errors: FA_EINVAL, FA_ETOOBIG (more than 262,144 states, L >= 2^24),
+ * FA_ESTATE, FA_EHIP.
+ */
+int fa_beam_lookahead(const fa_table *t, int32_t L, uint32_t *sets, fa_stream_t stream);
+
+/*
+ * fa_beam_start - the hypotheses before the first step: slot 0 of every row
+ * holds the empty string (score 0, the start state), the other slots none
+ * (score -inf, no state).
+ *   scores  device fp32 [B][K]; states device uint32 [B][K][W]
+ * Errors: FA_EINVAL, FA_ESTATE, FA_EHIP.
+ */
+int fa_beam_start(const fa_table *t, int32_t B, int32_t K, float *scores, uint32_t *states,
+                  fa_stream_t stream);
+
+/*
+ * fa_beam_select - one step of the search.  For every row b, hypothesis k of
+ * Kin with score s_k and state set Q_k, and token v that some edge out of Q_k
+ * holds (with a lookahead: an edge into a state of its row steps_left - 1),
+ *   key(k, v) = s_k + x_k[v] - ln sum_u exp x_k[u]   (FA_BEAM_LOGITS: the sum
+ *               runs over the whole vocabulary), or
+ *             = s_k + ln x_k[v]                      (FA_BEAM_PROBS)
+ * in fp64.  The K largest keys above -inf of the row are kept in descending
+ * order, ties to the lower k V + v; an NFA token counts once, whatever its
+ * number of paths.
+ *   dtype, logits   FA_F32, FA_F16 or FA_BF16; device; x_k[v] of row b at
+ *                   element b batch_stride + k beam_stride + v (strides >= 0;
+ *                   beam_stride 0: one row shared by the hypotheses)
+ *   scores_in       device fp32 [B][Kin]; -inf marks an empty slot, whose
+ *                   logits are not read
+ *   states_in       device uint32 [B][Kin][W]
+ *   lookahead       device, from fa_beam_lookahead, or NULL (steps_left 0)
+ *   steps_left      tokens still to come, this one included (1..L of the
+ *                   lookahead): the last step's hypotheses end in F
+ *   scores, tokens, parents  device fp32, int32, int32 [B][K]; states device
+ *                   uint32 [B][K][W]: per kept hypothesis the key rounded to
+ *                   fp32, v, k, and the states its tokens lead to (with a
+ *                   lookahead those of its row steps_left - 1).  A slot
+ *                   without a hypothesis gets -inf, -1, its own index modulo
+ *                   Kin, and no state.  Not the input buffers.
+ *   ws              device workspace (fa_beam_sizes; 16-byte aligned)
+ *   row_status      device int32 [B], read and OR-ed: FA_ROW_BADPROB (a NaN or
+ *                   +inf logit of a live hypothesis, a NaN, negative or
+ *                   infinite x_k[v] of a reachable token with FA_BEAM_PROBS, a
+ *                   score that is NaN or +inf), FA_ROW_INFEASIBLE (no key
+ *                   above -inf).  A row with a bit set, before the call or by
+ *                   it, gets K slots without a hypothesis.
+ * A captured call may be replayed; nothing depends on earlier contents of ws.
+ * Errors: FA_EINVAL (also a table without FA_BEAMS), FA_ETOOBIG (as
+ * fa_beam_sizes, or more than 2^31 - 1 workgroups), FA_ESTATE, FA_EHIP.
+ */
+int fa_beam_select(const fa_table *t, int32_t dtype, const void *logits, int64_t batch_stride,
+                   int64_t beam_stride, int32_t B, int32_t Kin, int32_t K, int32_t mode,
+                   const float *scores_in, const uint32_t *states_in, const uint32_t *lookahead,
+                   int32_t steps_left, float *scores, int32_t *tokens, int32_t *parents,
+                   uint32_t *states, void *ws, size_t ws_bytes, int32_t *row_status,
+                   fa_stream_t stream);
+
+/*
+ * fa_beam_reorder - per-hypothesis memory after the chosen parents: for every
+ * item and row b, slot k of dst becomes slot parents[b][k] of src.  Slot (b, k)
+ * of an item is `rows` pieces of row_bytes bytes: piece r at
+ * b batch_stride + k beam_stride + r row_stride bytes.  With dst == src (and
+ * the same strides) the item is reordered in place, whatever the parents
+ * (repeated, crossing), and slots that keep their place are not touched;
+ * otherwise the memory of src and dst must not overlap, and neither may the
+ * slots of one dst.  A parent outside 0..K-1 counts as the slot's own index.
+ *   items    host array, read during the call; pointers are device pointers
+ *   parents  device int32 [B][K], K in 1..FA_BEAM_MAX
+ * Errors: FA_EINVAL (sizes, null pointers, negative strides, dst == src with
+ * different strides), FA_ETOOBIG (2^32 or more 16-byte pieces in a slot, or
+ * 2^31 or more workgroups), FA_EHIP.
+ */
+typedef struct fa_beam_item {
+    const void *src;
+    void *dst;
+    int64_t src_batch_stride, src_beam_stride, src_row_stride; /* bytes */
+    int64_t dst_batch_stride, dst_beam_stride, dst_row_stride; /* bytes */
+    int64_t rows, row_bytes;
+} fa_beam_item;
+int fa_beam_reorder(const fa_beam_item *items, int32_t n_items, int32_t B, int32_t K,
+                    const int32_t *parents, fa_stream_t stream);
+
+/*
+ * fa_beam_trace - the hypotheses of T recorded steps:
+ *   out[b][k][t] = tokens[t][b][j_t],  j_{T-1} = k,  j_{t-1} = parents[t][b][j_t].
+ * Behind a parent outside 0..K-1 every earlier token of that hypothesis is -1.
+ *   tokens, parents  device int32 [T][B][K] (fa_beam_select's outputs of every
+ *                    step with Kin = K); out device int32 [B][K][T]
+ * Errors: FA_EINVAL, FA_ETOOBIG (T >= 2^24), FA_EHIP.
+ */
+int fa_beam_trace(int32_t T, int32_t B, int32_t K, const int32_t *tokens, const int32_t *parents,
+                  int32_t *out, fa_stream_t stream);
 
 /*
  * fa_span_tree_noalloc - fa_span_tree for callers that cannot allocate

@@ -1,0 +1,164 @@
+"""Host-side checks of the beam-search calls (no GPU): the refusals of the C
+entry points and of the binding, and FA_BEAMS in the table compiler."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import constrained_decoding_diffusion_amd as fa
+from constrained_decoding_diffusion_amd import _fa
+from synth import automata as A
+
+ONE = C.c_void_p(4096)    # a non-null pointer that nothing dereferences
+TWO = C.c_void_p(8192)
+
+
+def _table(beams=True, V=700, S=6, seed=1):
+    aut = A.random_dfa(np.random.default_rng(seed), S, V, 2, 0.4)
+    return fa.Table.from_automaton(aut, beams=beams)
+
+
+def test_flag_only_adds_to_the_image():
+    plain, beams = _table(False), _table(True)
+    assert plain.info["beams"] == 0 and beams.info["beams"] == 1
+    assert beams.device_bytes > plain.device_bytes
+    for k in plain.info:
+        assert k == "beams" or plain.info[k] == beams.info[k]
+
+
+def test_sizes():
+    tb = _table()
+    n, w = C.c_size_t(), C.c_int32()
+    L = fa.lib()
+    assert L.fa_beam_sizes(tb.handle, 3, 5, C.byref(n), C.byref(w)) == 0
+    assert w.value == 1 and n.value >= 3 * 5 * 2 * 4
+    assert L.fa_beam_sizes(tb.handle, 0, 1, None, None) == 0
+    for B, K in ((-1, 4), (1, 0), (1, 65), (1, -3)):
+        assert L.fa_beam_sizes(tb.handle, B, K, None, None) == _fa.FA_EINVAL
+    assert L.fa_beam_sizes(None, 1, 1, None, None) == _fa.FA_EINVAL
+    # 64 hypotheses of 262,144 tokens are the most the selection indexes
+    for V, K, rc in ((262144, 64, 0), (262145, 64, _fa.FA_ETOOBIG), (262145, 63, 0),
+                     (20_000_000, 1, _fa.FA_ETOOBIG)):
+        big = fa.Table(1, V, 0, [0], [0], [0], [0, 1], [V - 1], fa.FA_DFA | fa.FA_BEAMS)
+        assert L.fa_beam_sizes(big.handle, 1, K, None, None) == rc
+
+
+def _select(tb, **kw):
+    n = C.c_size_t()
+    fa.lib().fa_beam_sizes(tb.handle, 2, 4, C.byref(n), None)
+    a = dict(t=tb.handle, dtype=fa.FA_F32, logits=ONE, sb=2800, sk=700, B=2, Kin=4, K=4, mode=0,
+             scores_in=ONE, states_in=ONE, look=None, steps=0, scores=TWO, tokens=TWO, parents=TWO,
+             states=TWO, ws=ONE, ws_bytes=n.value, status=ONE, stream=None)
+    a.update(kw)
+    return fa.lib().fa_beam_select(*a.values())
+
+
+def test_select_refusals():
+    tb = _table()
+    assert _select(tb) == _fa.FA_ESTATE          # all is well but the table is not uploaded
+    assert _select(_table(False)) == _fa.FA_EINVAL
+    for kw in (dict(t=None), dict(dtype=3), dict(dtype=-1), dict(mode=2), dict(mode=-1),
+               dict(sb=-1), dict(sk=-700), dict(B=-1), dict(Kin=0), dict(Kin=65), dict(K=0),
+               dict(K=65), dict(logits=None), dict(scores_in=None), dict(states_in=None),
+               dict(scores=None), dict(tokens=None), dict(parents=None), dict(states=None),
+               dict(ws=None), dict(status=None), dict(ws_bytes=255), dict(ws=C.c_void_p(4100)),
+               dict(logits=C.c_void_p(4098)), dict(logits=C.c_void_p(4097), dtype=fa.FA_BF16),
+               dict(scores=ONE), dict(states=ONE), dict(steps=3), dict(look=ONE, steps=0),
+               dict(look=ONE, steps=-1)):
+        assert _select(tb, **kw) == _fa.FA_EINVAL, kw
+
+
+def test_lookahead_and_start_refusals():
+    tb, L = _table(), fa.lib()
+    assert L.fa_beam_lookahead(tb.handle, 4, ONE, None) == _fa.FA_ESTATE
+    assert L.fa_beam_lookahead(None, 4, ONE, None) == _fa.FA_EINVAL
+    assert L.fa_beam_lookahead(tb.handle, -1, ONE, None) == _fa.FA_EINVAL
+    assert L.fa_beam_lookahead(tb.handle, 4, None, None) == _fa.FA_EINVAL
+    assert L.fa_beam_lookahead(tb.handle, 1 << 24, ONE, None) == _fa.FA_ETOOBIG
+    assert L.fa_beam_start(tb.handle, 1, 4, ONE, ONE, None) == _fa.FA_ESTATE
+    for B, K, s, q in ((-1, 4, ONE, ONE), (1, 0, ONE, ONE), (1, 65, ONE, ONE), (1, 4, None, ONE),
+                       (1, 4, ONE, None)):
+        assert L.fa_beam_start(tb.handle, B, K, s, q, None) == _fa.FA_EINVAL
+
+
+def _item(**kw):
+    a = dict(src=4096, dst=1 << 20, src_batch_stride=64, src_beam_stride=16, src_row_stride=8,
+             dst_batch_stride=64, dst_beam_stride=16, dst_row_stride=8, rows=2, row_bytes=8)
+    a.update(kw)
+    return (_fa._BeamItem * 1)(_fa._BeamItem(*a.values()))
+
+
+def test_reorder_refusals():
+    f = fa.lib().fa_beam_reorder
+    # nothing to do
+    assert f(None, 0, 2, 4, None, None) == 0
+    assert f(_item(), 1, 0, 4, None, None) == 0
+    for n, B, K, par in ((-1, 2, 4, ONE), (1, -1, 4, ONE), (1, 2, 0, ONE), (1, 2, 65, ONE),
+                         (1, 2, 4, None)):
+        assert f(_item(), n, B, K, par, None) == _fa.FA_EINVAL
+    assert f(None, 1, 2, 4, ONE, None) == _fa.FA_EINVAL
+    for kw in (dict(src=None), dict(dst=None), dict(rows=-1), dict(row_bytes=-1),
+               dict(src_batch_stride=-1), dict(src_beam_stride=-1), dict(src_row_stride=-1),
+               dict(dst_batch_stride=-1), dict(dst_beam_stride=-1), dict(dst_row_stride=-1),
+               dict(dst_batch_stride=0), dict(dst_beam_stride=0), dict(dst_row_stride=7),
+               dict(dst=4096, dst_beam_stride=32), dict(dst=4096, src_batch_stride=128)):
+        assert f(_item(**kw), 1, 2, 4, ONE, None) == _fa.FA_EINVAL, kw
+    big = _item(rows=1 << 29, row_bytes=256, src_row_stride=256, dst_row_stride=256)
+    assert f(big, 1, 2, 4, ONE, None) == _fa.FA_ETOOBIG
+    # empty slots are nothing to move
+    assert f(_item(rows=0), 1, 2, 4, ONE, None) == 0
+    assert f(_item(row_bytes=0), 1, 2, 4, ONE, None) == 0
+
+
+def test_trace_refusals():
+    f = fa.lib().fa_beam_trace
+    assert f(0, 2, 4, None, None, None, None) == 0
+    assert f(5, 0, 4, None, None, None, None) == 0
+    for T, B, K, a, b, c in ((-1, 2, 4, ONE, ONE, ONE), (5, -1, 4, ONE, ONE, ONE),
+                             (5, 2, 0, ONE, ONE, ONE), (5, 2, 65, ONE, ONE, ONE),
+                             (5, 2, 4, None, ONE, ONE), (5, 2, 4, ONE, None, ONE),
+                             (5, 2, 4, ONE, ONE, None)):
+        assert f(T, B, K, a, b, c, None) == _fa.FA_EINVAL
+    assert f(1 << 24, 1, 4, ONE, ONE, ONE, None) == _fa.FA_ETOOBIG
+
+
+def test_binding_refuses_host_tensors_and_shapes():
+    tb = _table()
+    b = fa.BeamBuffers(tb, 2, 4, device="cpu")
+    good = torch.zeros(2, 4, 700)
+    for x in (good, good[:, :3], good[0], good[..., :699], good.double(), good.int()):
+        with pytest.raises(ValueError):
+            fa.beam_select(tb, x, b)
+    par = torch.zeros(2, 4, dtype=torch.int32)
+    for p in (par, par.long(), par[0], par.t()):
+        with pytest.raises(ValueError):
+            fa.beam_reorder([torch.zeros(2, 4, 3)], p)
+    h = torch.zeros(3, 2, 4, dtype=torch.int32)
+    for t, p in ((h, h), (h.long(), h.long()), (h[0], h[0])):
+        with pytest.raises(ValueError):
+            fa.beam_trace(t, p)
+    with pytest.raises(ValueError):
+        fa.beam_decode(tb, torch.zeros(2, 3, 700), 4)
+    with pytest.raises(ValueError):
+        fa.beam_search(tb, None, 1, 0, 4)
+
+
+@pytest.mark.parametrize("shape,view,want", [
+    ((2, 3, 5), lambda t: t, (1, 20, 20)),
+    ((2, 3), lambda t: t, (1, 4, 4)),
+    ((2, 3, 4, 10, 8), lambda t: t[:, :, :, :7], (4, 320, 224)),
+    ((2, 3, 2, 4, 10, 8), lambda t: t[:, :, :, :, :7], (8, 320, 224)),
+    ((2, 3, 4, 10, 8), lambda t: t[:, :, :, 2:3], (4, 320, 32)),
+    ((2, 3, 4, 10, 8), lambda t: t[:, :, 1:3, :, :5], (20, 32, 20)),
+    ((2, 3, 4, 0), lambda t: t, (0, 0, 0)),
+    ((2, 3, 6, 5), lambda t: t.transpose(2, 3), None),
+    ((2, 3, 4, 10, 8), lambda t: t[:, :, :, :7, :5], None),
+])
+def test_slot_rows(shape, view, want):
+    t = view(torch.zeros(shape))
+    if want is None:
+        with pytest.raises(ValueError):
+            _fa._slot_rows(t)
+    else:
+        assert _fa._slot_rows(t) == want

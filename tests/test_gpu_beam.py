@@ -1,0 +1,667 @@
+"""GPU parity of the beam-search operators against their fp64 definitions on
+the host (tests/beam_ref.py).
+
+Tolerance of the scores: the kernel's keys are fp64 sums of fp64 exponentials
+(relative error far below 1e-9) rounded once to fp32, so a score is off by at
+most half an fp32 step of its value, 2^-24 |score|, plus 1e-9.  Everything
+else (tokens, parents, states, status, moved bytes, hypotheses) is exact:
+logits are drawn so that candidates either tie exactly or lie further apart
+than that."""
+import numpy as np
+import pytest
+import torch
+
+import constrained_decoding_diffusion_amd as fa
+from synth import automata as A
+from tests import beam_ref as R
+from tests import parity as PT
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def _aut(kind, S, V, seed):
+    r = np.random.default_rng(seed)
+    if kind == "dfa":
+        return A.random_dfa(r, S, V, min(3, S), 0.3)
+    if kind == "json":
+        return A.json_like_dfa(r, S=S, V=V, pool=min(64, V // 4), max_struct=min(16, V // 4),
+                               string_size=(2 * V) // 3, n_accept=3)
+    if kind == "range":
+        return A.range_dfa(r, S=S, V=V, edges_per_state=min(8, V // 4))
+    if kind == "nfa":
+        return A.random_nfa(r, S, V, 8 * S, min(4, S), min(20.0, max(1.0, V / 4)))
+    if kind == "range-nfa":
+        return A.tiny_range_automaton(r, S, V, 6 * S, False)
+    return A.universal_automaton(V)
+
+
+def _table(aut, trim=True):
+    flags = (fa.FA_DFA if aut.dfa else fa.FA_NFA) | (fa.FA_LABEL_RANGES if aut.ranges else 0)
+    flags |= fa.FA_BEAMS | (0 if trim else fa.FA_NO_TRIM)
+    return fa.Table.from_automaton(aut, flags=flags)
+
+
+def _beams(tb, scores, sets, status=None):
+    """BeamBuffers of host scores [B, K] and sets of compact ids."""
+    B, K = scores.shape
+    b = fa.BeamBuffers(tb, B, K)
+    b.scores.copy_(torch.from_numpy(scores.astype(np.float32)))
+    b.states.copy_(torch.from_numpy(R.words_of(sets, b.words)))
+    if status is not None:
+        b.status.copy_(torch.from_numpy(status.astype(np.int32)))
+    return b
+
+
+def _reach(aut, r):
+    return A.accepting_reach_sets(aut, r)[r]
+
+
+def check(aut, x, scores, sets, K, mode="logits", steps=0, L=None, tb=None, what="", beams=None):
+    """x a cuda tensor [B, Kin, V]; a table that trims nothing, so that the
+    compact states are the automaton's own."""
+    PT.log(f"[beam] {what}: {aut.name} x {tuple(x.shape)} {x.dtype} K {K} {mode} steps {steps}")
+    tb = tb or _table(aut, trim=False)
+    beams = beams or _beams(tb, scores, sets)
+    out = fa.BeamBuffers(tb, x.shape[0], K)
+    for t in (out.scores, out.states, out.tokens, out.parents):
+        t.fill_(7)
+    ahead = fa.beam_lookahead(tb, L or steps) if steps else None
+    fa.beam_select(tb, x, beams, out=out, steps_left=steps, lookahead=ahead,
+                   mode=fa.FA_BEAM_PROBS if mode == "probs" else fa.FA_BEAM_LOGITS)
+    torch.cuda.synchronize()
+    reach = _reach(aut, steps - 1) if steps else None
+    sc, tok, par, new, status = R.select(aut, x.double().cpu().numpy(), scores.astype(np.float32),
+                                         sets, K, mode, reach)
+    np.testing.assert_array_equal(out.status.cpu().numpy(), status)
+    np.testing.assert_array_equal(out.tokens.cpu().numpy(), tok)
+    np.testing.assert_array_equal(out.parents.cpu().numpy(), par)
+    np.testing.assert_array_equal(out.states.cpu().numpy(), R.words_of(new, out.words))
+    got = out.scores.cpu().numpy().astype(np.float64)
+    live = sc > -np.inf
+    np.testing.assert_array_equal(got > -np.inf, live)
+    err = np.abs(got[live] - sc[live]) - 2.0 ** -24 * np.abs(sc[live])
+    assert err.size == 0 or err.max() <= 1e-9, err.max()
+    return out, new
+
+
+def _inputs(aut, B, K, dtype, seed, pad=0, spread=3.0, many=1):
+    r = np.random.default_rng(seed)
+    x = torch.from_numpy((r.normal(0, spread, (B, K, aut.V + pad))).astype(np.float32)).to(DT[dtype]).cuda()
+    scores = np.sort(-r.random((B, K)) * 5 - 3, -1)[:, ::-1].copy()
+    out = [s for s in range(aut.S) if (aut.src == s).any()] or [0]
+    sets = [[set(int(q) for q in r.choice(out, many)) for _ in range(K)] for _ in range(B)]
+    return x[:, :, :aut.V], scores, sets
+
+
+CASES = [
+    # kind, S, V, B, Kin, K, dtype, pad, many, steps
+    ("universal", 1, 1, 2, 1, 1, "f32", 0, 1, 0),
+    ("universal", 1, 1, 1, 4, 3, "bf16", 0, 1, 2),
+    ("dfa", 5, 7, 3, 2, 5, "f16", 0, 1, 0),
+    ("dfa", 9, 511, 2, 3, 3, "f32", 0, 1, 3),
+    ("dfa", 9, 512, 2, 3, 3, "bf16", 0, 1, 3),
+    ("dfa", 9, 513, 2, 3, 3, "f16", 3, 1, 3),
+    ("dfa", 33, 2047, 2, 16, 16, "bf16", 1, 1, 4),
+    ("dfa", 40, 2049, 1, 17, 17, "bf16", 0, 1, 0),
+    ("dfa", 64, 5003, 2, 64, 64, "f32", 5, 1, 5),
+    ("json", 40, 9001, 3, 8, 8, "bf16", 0, 1, 0),
+    ("json", 40, 9001, 3, 8, 8, "f16", 7, 1, 6),
+    ("json", 96, 40000, 2, 5, 7, "f32", 0, 1, 9),
+    ("json", 64, 16384, 2, 8, 33, "bf16", 64, 2, 5),
+    ("range", 12, 100, 2, 4, 4, "f32", 0, 1, 3),
+    ("range", 70, 20011, 2, 9, 9, "bf16", 5, 1, 4),
+    ("range", 70, 20011, 1, 64, 64, "f16", 0, 1, 4),
+    ("nfa", 40, 300, 2, 4, 4, "f32", 0, 1, 3),
+    ("nfa", 300, 4100, 2, 12, 20, "bf16", 0, 6, 4),
+    ("nfa", 2500, 3001, 1, 6, 6, "f16", 0, 40, 0),
+    ("range-nfa", 20, 900, 3, 5, 5, "f32", 0, 3, 3),
+    ("range-nfa", 20, 4500, 2, 3, 40, "bf16", 0, 5, 0),
+    ("dfa", 6, 70000, 1, 64, 64, "f32", 0, 1, 3),
+]
+
+
+@pytest.mark.parametrize("i", range(len(CASES)))
+@pytest.mark.parametrize("mode", ["logits", "probs"])
+def test_select(i, mode):
+    kind, S, V, B, Kin, K, dtype, pad, many, steps = CASES[i]
+    aut = _aut(kind, S, V, 100 + i)
+    x, scores, sets = _inputs(aut, B, Kin, dtype, 200 + i, pad, many=many)
+    if mode == "probs":
+        x = torch.softmax(x.float(), -1).to(x.dtype)
+        if pad:
+            x = torch.cat([x, x[..., :pad]], -1)[..., :V]
+    check(aut, x, scores, sets, K, mode, steps, what=f"case {i}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("mode", ["logits", "probs"])
+def test_select_shared_row_and_strides(dtype, mode):
+    """One row for all hypotheses (stride 0), hypotheses further apart than
+    batch rows, a base address that is not 16-byte aligned."""
+    aut = _aut("json", 40, 9001, 5)
+    B, K = 2, 6
+    r = np.random.default_rng(6)
+    z = torch.from_numpy(r.normal(0, 2, (B, 9001)).astype(np.float32)).cuda()
+    z = (torch.softmax(z, -1) if mode == "probs" else z).to(DT[dtype])
+    _, scores, sets = _inputs(aut, B, K, "f32", 7)
+    check(aut, z[:, None].expand(B, K, 9001), scores, sets, K, mode, 4, what="shared")
+    buf = torch.zeros(K, B, 9100, dtype=DT[dtype], device="cuda")
+    view = buf.transpose(0, 1)[:, :, 3:9004]
+    view.copy_(z[:, None] * torch.linspace(0.9, 1.0, K, device="cuda")[None, :, None])
+    check(aut, view, scores, sets, K, mode, 4, what="transposed")
+    # one row for batch and hypotheses
+    check(aut, z[:1, None].expand(B, K, 9001), scores, sets, K, mode, 4, what="one row")
+
+
+@pytest.mark.parametrize("K", [1, 3, 16, 17, 64])
+@pytest.mark.parametrize("mode", ["logits", "probs"])
+def test_select_ties_go_to_the_lowest_index(K, mode):
+    """Constant rows and equal scores: every candidate ties, within a granule,
+    across granules and across hypotheses."""
+    aut = _aut("universal", 1, 1537, 0)
+    for Kin in (1, 4):
+        x = torch.full((2, Kin, 1537), 0.25, device="cuda")
+        scores = np.full((2, Kin), -2.0)
+        scores[1] -= np.arange(Kin) % 2
+        check(aut, x, scores, [[{0}] * Kin] * 2, K, mode, what="ties")
+    # two values only, coarse in bf16
+    r = np.random.default_rng(K)
+    x = torch.from_numpy(r.integers(0, 2, (2, 4, 1537)).astype(np.float32) / 4 + 0.25).bfloat16().cuda()
+    check(aut, x, np.full((2, 4), -1.0), [[{0}] * 4] * 2, K, mode, what="two values")
+
+
+def test_select_few_candidates_and_empty_sets():
+    """Fewer candidates than slots, hypotheses without states or without
+    out-edges, empty slots, rows with nothing at all."""
+    aut = A._pack(4, 600, 0, [2], [(0, 1, [5, 599]), (1, 2, [0]), (1, 3, [1])], name="hand")
+    x, _, _ = _inputs(aut, 5, 3, "f32", 3)
+    sets = [[{0}, {1}, {2}], [{3}, {2}, set()], [{0}, {0}, {0}], [{1}, set(), {0}], [set()] * 3]
+    scores = np.array([[-1, -2, -3], [-1, -2, -3], [-np.inf, -1, -np.inf], [-np.inf] * 3,
+                       [0, 0, 0]], np.float64)
+    out, _ = check(aut, x, scores, sets, 4, what="few")
+    assert out.status.tolist() == [0, 1, 0, 1, 1]
+    # the last step: targets accept; state 3 does not
+    out, _ = check(aut, x, scores, sets, 4, steps=1, what="last step")
+    assert out.tokens[0].tolist() == [0, -1, -1, -1]
+    # two steps before the end state 1 leads nowhere that accepts in one step
+    check(aut, x, scores, sets, 4, steps=2, L=5, what="two left")
+
+
+def test_select_masked_values():
+    """-inf logits are tokens without a key, the type's lowest value is a
+    value; all -inf, or NaN and infinities where nothing may be read."""
+    aut = _aut("dfa", 6, 1300, 8)
+    for dtype in DT:
+        x, scores, sets = _inputs(aut, 3, 4, dtype, 9)
+        x = x.clone()
+        x[0, 0, 100:1200] = -float("inf")
+        x[0, 1] = -float("inf")
+        x[1, 2, 5:] = torch.finfo(DT[dtype]).min
+        x[1, 3] = torch.finfo(DT[dtype]).min
+        scores[2, 1] = -np.inf
+        x[2, 1] = float("nan")        # an empty slot's logits are not read
+        check(aut, x, scores, sets, 6, steps=3, what=f"-inf {dtype}")
+        x[2] = -float("inf")
+        out, _ = check(aut, x, scores, sets, 6, what=f"all -inf {dtype}")
+        assert out.status.tolist() == [0, 0, 1]
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_select_flags_bad_logits(value):
+    aut = _aut("json", 20, 9001, 8)
+    for at in (0, 4099, 9000):
+        x, scores, sets = _inputs(aut, 3, 4, "f32", 9)
+        x = x.clone()
+        x[1, 2, at] = value
+        out, _ = check(aut, x, scores, sets, 4, what=f"{value} at {at}")
+        assert out.status.tolist() == [0, 4, 0]
+        assert (out.scores[1] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -1e-30])
+def test_select_probs_flags_only_reachable_tokens(value):
+    aut = A._pack(2, 1100, 0, [1], [(0, 1, np.arange(0, 1100, 2)), (0, 0, [1])], name="even")
+    x, scores, _ = _inputs(aut, 3, 2, "f32", 9)
+    x = torch.softmax(x, -1)
+    x[0, 0, 701] = value              # no edge holds 701
+    x[1, 1, 702] = value
+    out, _ = check(aut, x, scores, [[{0}, {0}]] * 3, 3, "probs", what=f"probs {value}")
+    assert out.status.tolist() == [0, 4, 0]
+    # under the lookahead token 1's target does not accept in zero steps
+    x[1, 1, 702] = 0.5
+    x[2, 0, 1] = value
+    out, _ = check(aut, x, scores, [[{0}, {0}]] * 3, 3, "probs", steps=1, what="probs last")
+    assert out.status.tolist() == [0, 0, 0]
+
+
+def test_select_zero_probabilities():
+    aut = _aut("universal", 1, 800, 0)
+    x = torch.zeros(2, 2, 800, device="cuda")
+    x[0, 1, 5] = 0.25
+    x[0, 0, 799] = 1e-44              # a subnormal number is a probability
+    out, _ = check(aut, x, np.array([[-1.0, -3.0], [-1.0, -3.0]]), [[{0}, {0}]] * 2, 3, "probs")
+    assert out.status.tolist() == [0, 1] and out.tokens[0].tolist() == [5, 799, -1]
+
+
+def test_select_bad_scores_and_flagged_rows():
+    aut = _aut("dfa", 6, 700, 8)
+    x, scores, sets = _inputs(aut, 4, 3, "f32", 9)
+    scores[0, 1] = np.nan
+    scores[1, 2] = np.inf
+    out, _ = check(aut, x, scores, sets, 3, what="bad scores")
+    assert out.status.tolist() == [4, 4, 0, 0]
+    # a row flagged before the call stays flagged and empty
+    x, scores, sets = _inputs(aut, 4, 3, "f32", 9)
+    tb = _table(aut, trim=False)
+    beams = _beams(tb, scores, sets, np.array([0, 2, 0, 1]))
+    out = fa.beam_select(tb, x, beams)
+    assert out.status.tolist() == [0, 2, 0, 1]
+    for b in (1, 3):
+        assert (out.tokens[b] == -1).all() and (out.states[b] == 0).all()
+        assert (out.scores[b] == -float("inf")).all() and out.parents[b].tolist() == [0, 1, 2]
+    assert (out.tokens[0] >= 0).all() and (out.tokens[2] >= 0).all()
+
+
+def test_select_far_offsets():
+    """Rows more than 2^32 bytes apart."""
+    aut = _aut("dfa", 6, 700, 8)
+    big = torch.empty((2, 2, 1 << 30), dtype=torch.bfloat16, device="cuda")
+    x = big[:, :, (1 << 30) - 700:]
+    y, scores, sets = _inputs(aut, 2, 2, "bf16", 9)
+    x.copy_(y)
+    check(aut, x, scores, sets, 4, steps=3, what="far")
+
+
+def test_select_large_vocabularies():
+    """The largest vocabulary with the most hypotheses, and a larger one."""
+    V = 262144
+    aut = A._pack(2, V, 0, [0], [(0, 0, [0, V // 2]), (0, 1, [V // 2, V]), (1, 0, [17, V - 1])],
+                  ranges=True, name="halves")
+    tb = _table(aut, trim=False)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn((1, 64, V), generator=g, device="cuda")
+    scores = np.linspace(-1, -9, 64)[None]
+    check(aut, x, scores, [[{k % 2} for k in range(64)]], 64, tb=tb, what="262144 x 64")
+    V = 1_000_001
+    aut = A._pack(1, V, 0, [0], [(0, 0, [0, V])], ranges=True, name="one million")
+    x = torch.randn((1, 2, V), generator=g, device="cuda").bfloat16()
+    check(aut, x, np.array([[-1.0, -1.5]]), [[{0}, {0}]], 5, what="a million tokens")
+
+
+def test_lookahead_and_start():
+    for kind, S, V in (("dfa", 40, 200), ("nfa", 300, 500), ("range", 20, 90), ("json", 33, 4000)):
+        aut = _aut(kind, S, V, 50)
+        for trim in (True, False):
+            tb = _table(aut, trim)
+            L = 40
+            got = fa.beam_lookahead(tb, L).cpu().numpy()
+            want = A.accepting_reach_sets(aut, L)[:, tb.orig]
+            np.testing.assert_array_equal(
+                got, R.words_of([[set(np.flatnonzero(w).tolist())] for w in want], got.shape[1])[:, 0])
+            b = fa.beam_start(tb, 3, 5)
+            assert b.scores.tolist() == [[0.0] + [-float("inf")] * 4] * 3
+            start = int(np.flatnonzero(tb.orig == aut.start)[0])
+            np.testing.assert_array_equal(
+                b.states.cpu().numpy(), R.words_of([[{start}] + [set()] * 4] * 3, b.words))
+            assert b.status.tolist() == [0] * 3
+    # a cycle of three states: the sets never settle
+    aut = A._pack(3, 4, 0, [0], [(0, 1, [0]), (1, 2, [1]), (2, 0, [2])], name="cycle")
+    got = fa.beam_lookahead(_table(aut), 7).cpu().numpy()[:, 0]
+    assert got.tolist() == [1, 4, 2, 1, 4, 2, 1, 4]
+    assert fa.beam_lookahead(_table(aut), 0).cpu().numpy()[:, 0].tolist() == [1]
+
+
+# ------------------------------------------------------------------ reorder
+REORDER = [
+    # B, K, inner shape, view, dtype
+    (1, 1, (5,), lambda t: t, torch.float32),
+    (2, 3, (), lambda t: t, torch.int64),
+    (2, 4, (7,), lambda t: t, torch.bfloat16),
+    (3, 5, (3, 33, 5), lambda t: t[:, :, :, :29], torch.uint8),
+    (2, 8, (4, 40, 64), lambda t: t[:, :, :, :33], torch.bfloat16),
+    (2, 9, (4, 40, 24), lambda t: t[:, :, :, 3:40], torch.float16),
+    (1, 17, (2, 70, 20), lambda t: t[:, :, :, :1], torch.float32),
+    (2, 33, (3, 20, 9), lambda t: t[:, :, :, 1:], torch.uint8),
+    (1, 64, (2, 50, 80), lambda t: t[:, :, :, :41], torch.bfloat16),
+    (2, 6, (1, 1, 100003), lambda t: t, torch.uint8),
+    (2, 6, (31,), lambda t: t.transpose(0, 1).contiguous().transpose(0, 1), torch.float32),
+]
+
+
+def _filled(shape, dtype, r):
+    n = int(np.prod(shape))
+    if dtype.is_floating_point:
+        return torch.from_numpy(r.normal(0, 1, n).astype(np.float32)).to(dtype).reshape(shape).cuda()
+    return torch.from_numpy(r.integers(0, 200, n)).to(dtype).reshape(shape).cuda()
+
+
+def _parents(r, B, K, kind):
+    if kind == "random":
+        return r.integers(0, K, (B, K))
+    if kind == "cycle":
+        return np.stack([np.roll(np.arange(K), b + 1) for b in range(B)])
+    if kind == "one":
+        return np.full((B, K), K - 1)
+    if kind == "same":
+        return np.tile(np.arange(K), (B, 1))
+    p = r.integers(-2, K + 2, (B, K))       # some out of range: they keep their slot
+    p[0, 0] = -(1 << 31)
+    p[-1, -1] = (1 << 31) - 1
+    return p
+
+
+@pytest.mark.parametrize("kind", ["random", "cycle", "one", "same", "range"])
+@pytest.mark.parametrize("i", range(len(REORDER)))
+def test_reorder(i, kind):
+    B, K, inner, view, dtype = REORDER[i]
+    r = np.random.default_rng(30 + i)
+    par = _parents(r, B, K, kind)
+    p = torch.from_numpy(par.astype(np.int32)).cuda()
+    full = _filled((B, K) + inner, dtype, r)
+    PT.log(f"[beam] reorder {i} {kind} {tuple(full.shape)} {dtype}")
+    # into a second buffer whose other parts stay as they were
+    src = view(full)
+    other = view(torch.full_like(full, 3))
+    before = full.clone()
+    fa.beam_reorder([src], p, out=[other])
+    want = torch.from_numpy(R.reorder(src.cpu().float().numpy(), par))
+    assert torch.equal(other.cpu().float(), want)
+    assert torch.equal(full, before)
+    # in place; what lies outside the view stays
+    expect = before.clone()
+    view(expect).copy_(other)
+    target = view(full)
+    if target.data_ptr() == full.data_ptr() and target.shape == full.shape and target.stride() != full.stride():
+        full = target
+        expect = other
+    fa.beam_reorder([target], p)
+    assert torch.equal(target, other)
+    assert torch.equal(full, expect)
+
+
+def test_reorder_many_tensors_at_once():
+    """More tensors than one launch takes, of all types and sizes, some empty."""
+    r = np.random.default_rng(2)
+    B, K = 2, 5
+    ts = []
+    for i in range(70):
+        inner = [(3, 11, 16), (7,), (2, 1), (0, 4), ()][i % 5]
+        ts.append(_filled((B, K) + inner, [torch.float32, torch.uint8, torch.bfloat16][i % 3], r))
+    par = _parents(r, B, K, "random")
+    want = [R.reorder(t.cpu().float().numpy(), par) for t in ts]
+    out = fa.beam_reorder(ts, torch.from_numpy(par.astype(np.int32)).cuda())
+    assert out is ts
+    for t, w in zip(ts, want):
+        np.testing.assert_array_equal(t.cpu().float().numpy(), w)
+    assert fa.beam_reorder([], torch.zeros(2, 5, dtype=torch.int32, device="cuda")) == []
+    # a strided source into a contiguous buffer
+    src = _filled((B, K, 4, 10, 6), torch.float32, r)[:, :, :, :7]
+    dst = torch.empty((B, K, 4, 7, 6), device="cuda")
+    fa.beam_reorder([src], torch.from_numpy(par.astype(np.int32)).cuda(), out=[dst])
+    np.testing.assert_array_equal(dst.cpu().numpy(), R.reorder(src.cpu().numpy(), par))
+
+
+def test_reorder_far_offsets():
+    """Slots more than 2^32 bytes apart."""
+    big = torch.empty((2, 2, (1 << 32) + 64), dtype=torch.uint8, device="cuda")
+    v = big[..., (1 << 32):]
+    v.copy_(torch.arange(4 * 64, device="cuda").reshape(2, 2, 64) % 251)
+    want = v.clone()[:, [1, 0]]
+    fa.beam_reorder([v], torch.tensor([[1, 0], [1, 0]], dtype=torch.int32, device="cuda"))
+    assert torch.equal(v, want)
+
+
+def test_reorder_refusals():
+    p = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    t = torch.zeros(2, 3, 4, 5, device="cuda")
+    for bad in (t[:, :2], t[0], t.cpu(), t.transpose(2, 3), t[:, :, :, :1].expand(2, 3, 4, 6).transpose(2, 3)):
+        with pytest.raises(ValueError):
+            fa.beam_reorder([bad], p)
+    for out in ([t.half()], [t[..., :4]], [t, t], [t.cpu()]):
+        with pytest.raises(ValueError):
+            fa.beam_reorder([t], p, out=out)
+    with pytest.raises(fa.FaError):
+        fa.beam_reorder([t], p, out=[t[:, :1].expand(2, 3, 4, 5)])
+    with pytest.raises(fa.FaError):
+        fa.beam_reorder([torch.zeros(1, 65, 2, device="cuda")],
+                        torch.zeros(1, 65, dtype=torch.int32, device="cuda"))
+
+
+# -------------------------------------------------------------------- trace
+@pytest.mark.parametrize("T,B,K", [(1, 1, 1), (1, 3, 4), (2, 2, 3), (33, 2, 5), (64, 1, 64),
+                                   (257, 3, 7), (1000, 2, 16), (4099, 1, 64), (5000, 2, 2)])
+def test_trace(T, B, K):
+    r = np.random.default_rng(T)
+    PT.log(f"[beam] trace T {T} B {B} K {K}")
+    tok = r.integers(-1, 1000, (T, B, K)).astype(np.int32)
+    par = r.integers(0, K, (T, B, K)).astype(np.int32)
+    got = fa.beam_trace(torch.from_numpy(tok).cuda(), torch.from_numpy(par).cuda()).cpu().numpy()
+    np.testing.assert_array_equal(got, R.trace(tok, par))
+    # parents out of range end a hypothesis
+    bad = par.copy()
+    for _ in range(max(1, T // 50)):
+        bad[r.integers(T), r.integers(B), r.integers(K)] = [-1, K, 1 << 30][r.integers(3)]
+    got = fa.beam_trace(torch.from_numpy(tok).cuda(), torch.from_numpy(bad).cuda()).cpu().numpy()
+    np.testing.assert_array_equal(got, R.trace(tok, bad))
+
+
+def test_trace_empty():
+    z = torch.zeros(0, 2, 3, dtype=torch.int32, device="cuda")
+    assert fa.beam_trace(z, z).shape == (2, 3, 0)
+    z = torch.zeros(4, 0, 3, dtype=torch.int32, device="cuda")
+    assert fa.beam_trace(z, z).shape == (0, 3, 4)
+
+
+# ----------------------------------------------------------------- together
+@pytest.mark.parametrize("kind,S,V,K,L", [("dfa", 20, 300, 4, 9), ("json", 40, 9001, 8, 12),
+                                          ("range", 16, 700, 5, 7), ("nfa", 60, 400, 6, 8)])
+def test_search(kind, S, V, K, L):
+    """A whole search with a model that has a memory per hypothesis: logits
+    that depend on the hypothesis' own tokens, kept in a cache that the
+    search reorders.  Every string ends in an accepting state."""
+    aut = _aut(kind, S, V, 71)
+    B = 2
+    if not _reach(aut, L)[aut.start]:
+        pytest.skip("no accepted string of this length")
+    r = np.random.default_rng(72)
+    E = torch.from_numpy(r.normal(0, 1, (V, 16)).astype(np.float32)).cuda()
+    W = torch.from_numpy(r.normal(0, 1, (16, V)).astype(np.float32)).cuda()
+    pos = torch.from_numpy(r.normal(0, 1, (L, B, 1, V)).astype(np.float32)).cuda()
+    cache = torch.zeros(B, K, 16, device="cuda")
+    seen = torch.full((B, K, L), -1, dtype=torch.int32, device="cuda")
+    log = []
+
+    def model(t, tokens):
+        if t:
+            cache.mul_(0.5).add_(E[tokens.clamp(min=0).long()])
+            seen[:, :, t - 1] = tokens
+        x = cache.double() @ W.double() + pos[t]
+        log.append(x.float())
+        return x.float()
+
+    tb = _table(aut)
+    hyp, beams = fa.beam_search(tb, model, B, L, K, caches=[cache, seen])
+    torch.cuda.synchronize()
+    PT.log(f"[beam] search {aut.name}: scores {beams.scores.tolist()}")
+    assert beams.status.tolist() == [0] * B
+    R_ = A.accepting_reach_sets(aut, L)
+    logits = [x.double().cpu().numpy() for x in log]
+    tok, scores, status = R.search(aut, lambda t, a, b: logits[t], B, L, K, R_)
+    np.testing.assert_array_equal(status, 0)
+    live = scores > -np.inf
+    got = hyp.cpu().numpy()
+    np.testing.assert_array_equal(got[live], tok[live])
+    assert (got[~live] == -1).all()
+    # L roundings of at most half a step each
+    np.testing.assert_allclose(beams.scores.cpu().numpy()[live], scores[live],
+                               rtol=L * 2.0 ** -24, atol=1e-9)
+    # the cache followed: every hypothesis' own tokens but the last, in its slot
+    np.testing.assert_array_equal(seen.cpu().numpy()[live][:, :L - 1], got[live][:, :-1])
+    edges = R.edge_tokens(aut)
+    acc = set(aut.accept.tolist())
+    for b in range(B):
+        for k in np.flatnonzero(live[b]):
+            q = {aut.start}
+            for v in got[b, k]:
+                q = {to for s in q for lab, to in edges[s] if v in lab}
+            assert q & acc
+        strings = [tuple(got[b, k]) for k in np.flatnonzero(live[b])]
+        assert len(set(strings)) == len(strings)
+
+
+def test_decode_agrees_with_map_and_enumeration():
+    """beam_decode with more hypotheses than the automaton has prefixes is
+    exhaustive: its strings are the K best by enumeration, and the first is
+    map_decode's."""
+    aut = A.real_number_dfa()
+    L, B, K = 4, 3, 64
+    r = np.random.default_rng(5)
+    # six usable tokens keep the prefixes of length 3 below 64
+    p = r.dirichlet(np.ones(12), (B, L)).astype(np.float32)
+    keep = [0, 3, 7, 10]
+    z = np.zeros_like(p)
+    z[..., keep] = p[..., keep]
+    p = torch.from_numpy(z).cuda()
+    tb = _table(aut)
+    hyp, beams = fa.beam_decode(tb, p, K)
+    mp = fa.map_decode(tb, p)
+    torch.cuda.synchronize()
+    import itertools
+    edges = R.edge_tokens(aut)
+    for b in range(B):
+        every = []
+        for s in itertools.product(keep, repeat=L):
+            q = {aut.start}
+            for v in s:
+                q = {to for a in q for lab, to in edges[a] if v in lab}
+            if q & set(aut.accept.tolist()):
+                every.append((sum(np.log(float(z[b, i, v])) for i, v in enumerate(s)), s))
+        every.sort(key=lambda e: -e[0])
+        n = min(K, len(every))
+        got = [tuple(h) for h in hyp[b, :n].cpu().tolist()]
+        assert got == [s for _, s in every[:n]]
+        np.testing.assert_allclose(beams.scores[b, :n].cpu().numpy(), [e for e, _ in every[:n]],
+                                   rtol=L * 2.0 ** -24)
+        assert got[0] == tuple(mp.tokens[b].cpu().tolist())
+        assert beams.scores[b, 0].item() == pytest.approx(mp.logmax[b].item(), rel=1e-6)
+
+
+def test_decode_flags_infeasible_rows():
+    aut = A.single_string_automaton([3, 1, 2], 8)
+    p = torch.full((2, 3, 8), 0.125, device="cuda")
+    p[1, 1] = 0
+    p[1, 1, 5] = 1
+    hyp, beams = fa.beam_decode(_table(aut), p, 3)
+    assert beams.status.tolist() == [0, 1]
+    assert hyp.tolist() == [[[3, 1, 2], [-1] * 3, [-1] * 3], [[-1] * 3] * 3]
+
+
+# --------------------------------------------------------- streams, graphs
+def test_two_streams_and_a_table_shared():
+    aut = _aut("json", 40, 30011, 8)
+    tb = _table(aut, trim=False).upload()
+    torch.cuda.synchronize()
+    args = [_inputs(aut, 4, 8, "bf16", 90 + i) for i in range(2)]
+    refs = [fa.beam_select(tb, x, _beams(tb, s, q)) for x, s, q in args]
+    beams = [_beams(tb, s, q) for _, s, q in args]
+    outs = [fa.BeamBuffers(tb, 4, 8) for _ in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, (x, _, _), b, o in zip(streams, args, beams, outs):
+            with torch.cuda.stream(st):
+                fa.beam_select(tb, x, b, out=o)
+        torch.cuda.synchronize()
+        for o, ref in zip(outs, refs):
+            for f in ("scores", "tokens", "parents", "states"):
+                assert torch.equal(getattr(o, f), getattr(ref, f))
+
+
+def test_captured_step_replays():
+    """Select, reorder and trace captured once, replayed on new inputs with
+    eager work and synchronizations between; two graphs share the workspace."""
+    aut = _aut("json", 40, 30011, 8)
+    tb = _table(aut, trim=False).upload()
+    ahead = fa.beam_lookahead(tb, 9)
+    x, s, q = _inputs(aut, 3, 6, "bf16", 91)
+    x = x.contiguous()
+    beams = _beams(tb, s, q)
+    out = fa.BeamBuffers(tb, 3, 6, like=beams)
+    out2 = fa.BeamBuffers(tb, 3, 6, like=beams)
+    cache = torch.randn(3, 6, 2, 50, 33, device="cuda")
+    moved = torch.zeros_like(cache)
+    tok = torch.randint(0, 99, (20, 3, 6), dtype=torch.int32, device="cuda")
+    par = torch.randint(0, 6, (20, 3, 6), dtype=torch.int32, device="cuda")
+
+    def work(o, steps):
+        fa.beam_select(tb, x, beams, out=o, steps_left=steps, lookahead=ahead)
+        fa.beam_reorder([cache], o.parents, out=[moved])
+        return fa.beam_trace(tok, par)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work(out, 5)
+        work(out2, 1)
+    torch.cuda.synchronize()
+    g, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hyp = work(out, 5)
+    with torch.cuda.graph(g2):
+        work(out2, 1)
+    for i in range(4):
+        y, s, q = _inputs(aut, 3, 6, "bf16", 92 + i)
+        x.copy_(y)
+        fresh = _beams(tb, s, q)
+        beams.scores.copy_(fresh.scores)
+        beams.states.copy_(fresh.states)
+        par.random_(0, 6)
+        g.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        for o, steps in ((out, 5), (out2, 1)):
+            want = fa.beam_select(tb, x, fresh, steps_left=steps, lookahead=ahead)
+            for f in ("scores", "tokens", "parents", "states"):
+                assert torch.equal(getattr(o, f), getattr(want, f)), (i, steps, f)
+            beams.status.zero_()
+        assert torch.equal(moved, fa.beam_reorder([cache], out2.parents, out=[torch.empty_like(cache)])[0])
+        assert torch.equal(hyp, fa.beam_trace(tok, par))
+
+
+def test_select_is_deterministic():
+    aut = _aut("nfa", 300, 4100, 8)
+    x, s, q = _inputs(aut, 4, 16, "f32", 12, many=5)
+    tb = _table(aut, trim=False)
+    b = _beams(tb, s, q)
+    first = fa.beam_select(tb, x, b)
+    for _ in range(5):
+        again = fa.beam_select(tb, x, b)
+        for f in ("scores", "tokens", "parents", "states"):
+            assert torch.equal(getattr(again, f), getattr(first, f))
+
+
+def test_select_binding_refusals():
+    aut = _aut("dfa", 9, 512, 1)
+    tb = _table(aut).upload()
+    x = torch.zeros(2, 3, 512, device="cuda")
+    b = fa.beam_start(tb, 2, 3)
+    ahead = fa.beam_lookahead(tb, 4)
+    for kw in (dict(steps_left=1), dict(steps_left=0, lookahead=ahead), dict(steps_left=5, lookahead=ahead),
+               dict(steps_left=1, lookahead=ahead[:, :0]), dict(out=b), dict(out=fa.BeamBuffers(tb, 1, 3)),
+               dict(steps_left=1, lookahead=ahead.cpu())):
+        with pytest.raises(ValueError):
+            fa.beam_select(tb, x, b, **kw)
+    for y in (x.double(), x[:, :2], x.transpose(1, 2).contiguous().transpose(1, 2), x.cpu()):
+        with pytest.raises(ValueError):
+            fa.beam_select(tb, y, b)
+    with pytest.raises(fa.FaError):
+        fa.beam_select(tb, x, b, mode=2)
+    with pytest.raises(fa.FaError):
+        fa.beam_start(tb, 2, 65)
+    plain = fa.Table.from_automaton(aut).upload()
+    with pytest.raises(fa.FaError):
+        fa.beam_select(plain, x, b)
+    fa.beam_select(tb, torch.zeros(0, 3, 512, device="cuda"), fa.BeamBuffers(tb, 0, 3))
