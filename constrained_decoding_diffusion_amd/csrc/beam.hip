@@ -130,7 +130,32 @@ __device__ inline const T *row_of(const BeamSelect &a, int row)
            (size_t)(row % a.Kin) * a.beam_stride;
 }
 
-// One wavefront: NG granules of one hypothesis.
+// 2^t for t in about [-1100, 1], to 2e-12 relative: the integer part by the
+// exponent, 2^f on [-1/2, 1/2] by its degree-8 interpolation at the Chebyshev
+// points.  fp64 fused multiply-adds run at the fp32 rate on this chip, and the
+// library's exp spends twice the operations on its last bits.
+__device__ inline double exp2_poly(double t)
+{
+    const double n = __builtin_rint(t);
+    const double f = t - n;
+    double r = 1.3255224878668817e-06;
+    r = fma(r, f, 1.5310079402249296e-05);
+    r = fma(r, f, 0.00015403455852453838);
+    r = fma(r, f, 0.0013333450568000645);
+    r = fma(r, f, 0.009618129159402558);
+    r = fma(r, f, 0.05550410941205933);
+    r = fma(r, f, 0.2402265069581299);
+    r = fma(r, f, 0.6931471805459335);
+    r = fma(r, f, 1.0);
+    return __builtin_ldexp(r, (int)n);
+}
+
+// One wavefront: NG granules of one hypothesis.  The logits are asked for
+// first and arrive while the mask is put together.
+//
+// The sum of exponentials is held in fp64 from the first term on: keys of
+// different hypotheses are compared with each other, and two of them may lie
+// closer than an fp32 sum over 150,000 tokens resolves.
 template <class T, int MODE, int NG>
 __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamSelect a,
                                                                float *__restrict__ gmax,
@@ -145,41 +170,52 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
     if (g0 >= nG) return;
     if (a.status[row / a.Kin] != 0 || a.scores_in[row] == -INFINITY) return;
     const T *x = row_of<T>(a, row);
+    float v[NG][8];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) load8(x, min((g0 + i) * kBeamGran + lane * 8, d.V), d.V, v[i]);
     uint32_t *mask = sh_mask[wave];
     allowed_mask(d, set_of(a, row, W), W, a.reach, g0, NG, mask, lane);
-    float v[NG][8];
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-        load8(x, min((g0 + i) * kBeamGran + lane * 8, d.V), d.V, v[i]);
         const uint32_t ok = (mask[i * kMaskWords + lane / 4] >> (8 * (lane & 3))) & 255u;
         float best = -INFINITY;
-        bool bad = false;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if ((ok >> j) & 1u) {
-                best = fmaxf(best, v[i][j]);
-                if (MODE == FA_BEAM_PROBS) bad |= !(v[i][j] >= 0.f && v[i][j] < INFINITY);
-            }
-            m = fmaxf(m, v[i][j]);
-        }
-        best = wave_max_f(best);
-        // a bad probability travels as a NaN maximum
-        if (MODE == FA_BEAM_PROBS && __ballot(bad)) best = NAN;
-        if (lane == 0 && g0 + i < nG) gmax[(size_t)row * nG + g0 + i] = best;
-    }
-    if (MODE == FA_BEAM_LOGITS) {
-        m = wave_max_f(m);
-        double s = 0.0;
-#pragma unroll
-        for (int i = 0; i < NG; ++i)
+        if (__ballot(ok != 0u)) {
+            bool bad = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float y = v[i][j];
-                if (m == -INFINITY) s += y != y ? (double)y : 0.0;  // nothing, or NaN alone
-                else s += exp((double)y - (double)m);
+                // the value where the bit is set, else -inf
+                const int on = (int)(ok << (31 - j)) >> 31;
+                const float y = __int_as_float((__float_as_int(v[i][j]) & on) | (~on & (int)0xff800000));
+                best = fmaxf(best, y);
+                if (MODE == FA_BEAM_PROBS) bad |= on && !(y >= 0.f && y < INFINITY);
             }
-        s = wave_sum_d(s);
+            best = wave_max_f(best);
+            // a bad probability travels as a NaN maximum
+            if (MODE == FA_BEAM_PROBS && __ballot(bad)) best = NAN;
+        }
+        if (lane == 0 && g0 + i < nG) gmax[(size_t)row * nG + g0 + i] = best;
+        if (MODE == FA_BEAM_LOGITS) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = __builtin_elementwise_maximum(m, v[i][j]);  // a NaN stays
+        }
+    }
+    if (MODE == FA_BEAM_LOGITS) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, o));
+        double s = m;  // NaN or +inf: the row is flagged
+        if (m == -INFINITY) s = 0.0;
+        else if (m < INFINITY) {
+            constexpr double kLog2e = 1.4426950408889634;
+            s = 0.0;
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    // the difference first: it is exact, whatever the size of the logits
+                    s += exp2_poly(fmax(((double)v[i][j] - (double)m) * kLog2e, -1100.0));
+            s = wave_sum_d(s);
+        }
         if (lane == 0) part[(size_t)row * nG + chunk] = make_double2((double)m, s);
     }
 }
@@ -292,13 +328,18 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
             if (MODE == FA_BEAM_LOGITS && sc > -INFINITY && !bad) {
                 double m = -INFINITY, s = 0.0;
                 const double2 *pr = part + (size_t)(row0 + k) * nG;
-                for (int c = lane; c < chunks; c += kWave) m = fmax(m, pr[c].x);
+                bool odd = false;
+                for (int c = lane; c < chunks; c += kWave) {
+                    m = fmax(m, pr[c].x);
+                    odd |= !(pr[c].x < INFINITY);
+                }
                 m = wave_max_d(m);
                 for (int c = lane; c < chunks; c += kWave)
-                    s += pr[c].x == -INFINITY ? pr[c].y : pr[c].y * exp(pr[c].x - m);
+                    if (pr[c].x > -INFINITY) s += pr[c].y * exp(pr[c].x - m);
                 s = wave_sum_d(s);
-                lse = m == -INFINITY ? (s == 0.0 ? m : s) : m + log(s);
-                bad = !(lse < INFINITY);
+                if (m > -INFINITY) lse = m + log(s);
+                bad = __ballot(odd) != 0ull;
+                if (bad) lse = -INFINITY;
             }
             if (lane == 0) {
                 sh_lse[k] = lse;
