@@ -159,7 +159,8 @@ __device__ inline double exp2_poly(double t)
 template <class T, int MODE, int NG>
 __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamSelect a,
                                                                float *__restrict__ gmax,
-                                                               double2 *__restrict__ part, int nblk)
+                                                               double2 *__restrict__ part,
+                                                               uint32_t *__restrict__ gmask, int nblk)
 {
     __shared__ uint32_t sh_mask[kScanWaves][NG * kMaskWords];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -193,6 +194,9 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
             best = wave_max_f(best);
             // a bad probability travels as a NaN maximum
             if (MODE == FA_BEAM_PROBS && __ballot(bad)) best = NAN;
+            // for the second kernel, should the granule be among the best
+            if (best > -INFINITY && lane < kMaskWords)
+                gmask[((size_t)row * nG + g0 + i) * kMaskWords + lane] = mask[i * kMaskWords + lane];
         }
         if (lane == 0 && g0 + i < nG) gmax[(size_t)row * nG + g0 + i] = best;
         if (MODE == FA_BEAM_LOGITS) {
@@ -269,58 +273,154 @@ __device__ inline int wave_topk(double (&key)[R], Id id_of, int K, double *out_k
     return n;
 }
 
-// rank of every wavefront's candidates among all of them; those below K go to
-// their rank in out_key / out_id.  Returns how many there are (at most K).
-// Ends with the workgroup in step.
-__device__ inline int block_rank(const double *key, const uint32_t *id, const int *cnt, int K,
-                                 double *out_key, uint32_t *out_id)
+// ascending as x ascends; 0 for -inf (no key)
+__device__ inline uint32_t ordered_key(double x)
 {
+    if (!(x > -INFINITY)) return 0u;
+    const uint32_t u = __float_as_uint((float)x);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// the largest multiple of 2^10 that at least n (<= 64) lanes' values reach
+__device__ inline uint32_t nth_largest(uint32_t x, int n)
+{
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 10; --bit)
+        if (__popcll(__ballot(x >= (t | (1u << bit)))) >= n) t |= 1u << bit;
+    return t;
+}
+
+struct PickShared {
+    double key[kPickThreads];  // candidates
+    uint32_t id[kPickThreads];
+    double sel_key[FA_BEAM_MAX];  // the first K of them, in order
+    uint32_t sel_id[FA_BEAM_MAX];
+    int cnt[kPickWaves];
+    uint32_t tau[2][kPickWaves];
+    int n;  // candidates found, in either round
+    int n2;
+};
+
+// The candidates, unordered, in key / id: each ranked against all of them;
+// those below K go to their rank in sel_key / sel_id.
+__device__ inline void rank_candidates(PickShared &sh, int n, int K)
+{
+    if ((int)threadIdx.x < n) {
+        const double mk = sh.key[threadIdx.x];
+        const uint32_t mi = sh.id[threadIdx.x];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += before(sh.key[j], sh.id[j], mk, mi);
+        if (rank < K) {
+            sh.sel_key[rank] = mk;
+            sh.sel_id[rank] = mi;
+        }
+    }
+}
+
+// Where more candidates tie than the list holds: the wavefronts' own first K
+// one by one, and the rank of each among all wavefronts'.
+template <int R, class Id>
+__device__ inline int rank_by_rounds(PickShared &sh, double (&key)[R], Id id_of, int K, int lane,
+                                     int wave)
+{
+    const int c = wave_topk(key, id_of, K, sh.key + wave * FA_BEAM_MAX, sh.id + wave * FA_BEAM_MAX, lane);
+    if (lane == 0) sh.cnt[wave] = c;
     __syncthreads();
     int total = 0;
-    for (int w = 0; w < kPickWaves; ++w) total += cnt[w];
+    for (int w = 0; w < kPickWaves; ++w) total += sh.cnt[w];
     const int w0 = threadIdx.x / FA_BEAM_MAX, j0 = threadIdx.x % FA_BEAM_MAX;
-    if (j0 < cnt[w0]) {
-        const double mk = key[threadIdx.x];
-        const uint32_t mi = id[threadIdx.x];
+    if (j0 < sh.cnt[w0]) {
+        const double mk = sh.key[threadIdx.x];
+        const uint32_t mi = sh.id[threadIdx.x];
         int rank = 0;
         for (int w = 0; w < kPickWaves; ++w)
-            for (int j = 0; j < cnt[w]; ++j)
-                rank += before(key[w * FA_BEAM_MAX + j], id[w * FA_BEAM_MAX + j], mk, mi);
+            for (int j = 0; j < sh.cnt[w]; ++j)
+                rank += before(sh.key[w * FA_BEAM_MAX + j], sh.id[w * FA_BEAM_MAX + j], mk, mi);
         if (rank < K) {
-            out_key[rank] = mk;
-            out_id[rank] = mi;
+            sh.sel_key[rank] = mk;
+            sh.sel_id[rank] = mi;
         }
     }
     __syncthreads();
     return min(total, K);
 }
 
-// One workgroup: one batch row.  RG keys a lane hold the granules of its
-// hypotheses, RT those of the K granules' tokens.
-template <class T, int MODE, int RG, int RT>
+// appends the lanes' keys at or above the threshold to the candidate list;
+// counts all of them, also those past its end
+template <int R, class Take, class Id>
+__device__ inline void append(PickShared &sh, int *count, const double (&key)[R], Take take, Id id_of,
+                              int lane)
+{
+    unsigned long long hit[R];
+    int c = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        hit[r] = __ballot(take(r));
+        c += __popcll(hit[r]);
+    }
+    if (c == 0) return;
+    int base = 0;
+    if (lane == 0) base = atomicAdd(count, c);
+    base = __builtin_amdgcn_readfirstlane(base);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if ((hit[r] >> lane) & 1ull) {
+            const int at = base + __popcll(hit[r] & ((1ull << lane) - 1ull));
+            if (at < kPickThreads) {
+                sh.key[at] = key[r];
+                sh.id[at] = id_of(r);
+            }
+        }
+        base += __popcll(hit[r]);
+    }
+}
+
+__device__ inline void load8_as(int dtype, const void *row, int v, int V, float (&x)[8])
+{
+    if (dtype == FA_F32) load8(static_cast<const float *>(row), v, V, x);
+    else if (dtype == FA_F16) load8(static_cast<const _Float16 *>(row), v, V, x);
+    else load8(static_cast<const Bf16 *>(row), v, V, x);
+}
+
+// One workgroup: one batch row.  A lane holds RG granule maxima, and eight
+// tokens of RT granules a wavefront.
+//
+// Both rankings go by a threshold that at least K keys reach: every candidate
+// at or above it is listed, and each one's rank is the number of listed ones
+// before it, so no step of the work is repeated K times.  For the granules the
+// threshold is the better of two that the wavefronts' lane maxima give: the
+// largest of their K-th largest, and the smallest of their ceil(K/16)-th
+// largest.  For the tokens it is the K-th granule maximum.
+template <int MODE, int RG, int RT>
 __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect a,
                                                           const float *__restrict__ gmax,
                                                           const double2 *__restrict__ part,
+                                                          const uint32_t *__restrict__ gmask,
                                                           int chunks)
 {
     static_assert(kPickWaves * FA_BEAM_MAX == kPickThreads, "a thread per candidate slot");
     __shared__ double sh_lse[FA_BEAM_MAX];
-    __shared__ double sh_key[kPickThreads];
-    __shared__ uint32_t sh_id[kPickThreads];
-    __shared__ int sh_cnt[kPickWaves];
-    __shared__ double sel_key[FA_BEAM_MAX];
-    __shared__ uint32_t sel_id[FA_BEAM_MAX];
-    __shared__ uint32_t sh_mask[kPickWaves][kMaskWords];
+    __shared__ double sh_score[FA_BEAM_MAX];
+    __shared__ PickShared sh;
     __shared__ int sh_bad;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int nG = beam_grans(d.V), W = (d.S + 31) / 32, Kin = a.Kin, K = a.K;
-    const int row0 = b * Kin;
+    const int row0 = b * Kin, M = Kin * nG;
     const bool flagged = a.status[b] != 0;
-    if (tid == 0) sh_bad = 0;
-    if (tid < kPickWaves) sh_cnt[tid] = 0;
-    __syncthreads();
+    if (tid == 0) {
+        sh_bad = 0;
+        sh.n = 0;
+        sh.n2 = 0;
+    }
     int n = 0;
     if (!flagged) {
+        float gm[RG];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+            const int i = r * kPickThreads + tid;
+            gm[r] = i < M ? gmax[(size_t)row0 * nG + i] : -INFINITY;
+        }
+        __syncthreads();
         for (int k = wave; k < Kin; k += kPickWaves) {
             const float sc = a.scores_in[row0 + k];
             double lse = MODE == FA_BEAM_LOGITS ? -INFINITY : 0.0;
@@ -343,36 +443,65 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
             }
             if (lane == 0) {
                 sh_lse[k] = lse;
+                sh_score[k] = sc > -INFINITY ? (double)sc : -INFINITY;
                 if (bad) atomicOr(&sh_bad, 1);
             }
         }
         __syncthreads();
-        // the K granules with the largest keys
+        const uint32_t per_gran = nG > 1 ? 0xffffffffu / (uint32_t)nG + 1u : 0u;
+        // x the value of a token or of a granule's best one
+        auto key_of = [&](int k, float x) -> double {
+            const double sc = sh_score[k], lse = sh_lse[k];
+            if (!(x > -INFINITY) || !(sc > -INFINITY) || !(lse > -INFINITY)) return -INFINITY;
+            return MODE == FA_BEAM_PROBS ? sc + log((double)x) : sc + ((double)x - lse);
+        };
+        int ng;
         {
             double key[RG];
+            auto id_of = [&](int r) { return (uint32_t)(r * kPickThreads + tid); };
+            uint32_t top = 0;
             bool bad = false;
 #pragma unroll
             for (int r = 0; r < RG; ++r) {
-                const int i = r * kPickThreads + tid;
                 key[r] = -INFINITY;
-                if (i < Kin * nG) {
-                    const int k = i / nG;
-                    const double sc = a.scores_in[row0 + k], lse = sh_lse[k];
-                    if (sc > -INFINITY && lse > -INFINITY) {
-                        const double x = gmax[(size_t)row0 * nG + i];
-                        bad |= MODE == FA_BEAM_PROBS && x != x;
-                        if (x > -INFINITY) key[r] = MODE == FA_BEAM_PROBS ? sc + log(x) : sc + (x - lse);
+                const uint32_t i = id_of(r);
+                if (i < (uint32_t)M) {
+                    const int k = nG > 1 ? (int)__umulhi(i, per_gran) : (int)i;
+                    // a maximum of a hypothesis that was not scanned is not there
+                    if (sh_score[k] > -INFINITY) {
+                        bad |= MODE == FA_BEAM_PROBS && gm[r] != gm[r];
+                        key[r] = key_of(k, gm[r]);
                     }
                 }
+                top = max(top, ordered_key(key[r]));
             }
             if (bad) atomicOr(&sh_bad, 1);
-            const int c = wave_topk(key, [&](int r) { return (uint32_t)(r * kPickThreads + tid); },
-                                    K, sh_key + wave * FA_BEAM_MAX, sh_id + wave * FA_BEAM_MAX, lane);
-            if (lane == 0) sh_cnt[wave] = c;
+            const uint32_t most = nth_largest(top, K);
+            const uint32_t some = nth_largest(top, (K + kPickWaves - 1) / kPickWaves);
+            if (lane == 0) {
+                sh.tau[0][wave] = most;
+                sh.tau[1][wave] = some;
+            }
+            __syncthreads();
+            uint32_t hi = 0, lo = ~0u;
+            for (int w = 0; w < kPickWaves; ++w) {
+                hi = max(hi, sh.tau[0][w]);
+                lo = min(lo, sh.tau[1][w]);
+            }
+            const uint32_t tau = max(max(hi, lo), 1u);
+            append(sh, &sh.n, key, [&](int r) { return ordered_key(key[r]) >= tau; }, id_of, lane);
+            __syncthreads();
+            ng = sh.n;
+            if (ng <= kPickThreads) {
+                rank_candidates(sh, ng, K);
+                __syncthreads();
+                ng = min(ng, K);
+            } else {
+                ng = rank_by_rounds(sh, key, id_of, K, lane, wave);
+            }
         }
-        const int ng = block_rank(sh_key, sh_id, sh_cnt, K, sel_key, sel_id);
         // their tokens; none before the last of K granule maxima is lost
-        const double floor_key = ng == K ? sel_key[K - 1] : -INFINITY;
+        const double floor_key = ng == K ? sh.sel_key[K - 1] : -INFINITY;
         {
             double key[RT * 8];
             uint32_t base[RT];
@@ -383,29 +512,36 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
 #pragma unroll
                 for (int j = 0; j < 8; ++j) key[r * 8 + j] = -INFINITY;
                 if (q < ng) {
-                    const int i = sel_id[q], k = i / nG, g = i % nG;
-                    allowed_mask(d, set_of(a, row0 + k, W), W, a.reach, g, 1, sh_mask[wave], lane);
-                    const uint32_t ok = (sh_mask[wave][lane / 4] >> (8 * (lane & 3))) & 255u;
-                    const int v0 = g * kBeamGran + lane * 8;
+                    const uint32_t i = sh.sel_id[q];
+                    const int k = nG > 1 ? (int)__umulhi(i, per_gran) : (int)i;
+                    const int g = (int)i - k * nG, v0 = g * kBeamGran + lane * 8;
+                    const uint32_t ok = (gmask[((size_t)row0 * nG + i) * kMaskWords + lane / 4] >>
+                                         (8 * (lane & 3))) & 255u;
+                    const size_t at = (size_t)b * a.batch_stride + (size_t)k * a.beam_stride;
                     float x[8];
-                    load8(row_of<T>(a, row0 + k), min(v0, d.V), d.V, x);
-                    const double sc = a.scores_in[row0 + k], lse = sh_lse[k];
+                    load8_as(a.dtype, static_cast<const char *>(a.logits) + at * (a.dtype == FA_F32 ? 4 : 2),
+                             min(v0, d.V), d.V, x);
                     base[r] = (uint32_t)k * (uint32_t)d.V + (uint32_t)v0;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        double kk = -INFINITY;
-                        if (((ok >> j) & 1u) && x[j] > -INFINITY)
-                            kk = MODE == FA_BEAM_PROBS ? sc + log((double)x[j]) : sc + ((double)x[j] - lse);
+                        const double kk = (ok >> j) & 1u ? key_of(k, x[j]) : -INFINITY;
                         if (kk >= floor_key) key[r * 8 + j] = kk;
                     }
                 }
             }
+            __syncthreads();  // sel_* is read
+            auto id_of = [&](int r) { return base[r / 8] + (uint32_t)(r % 8); };
+            append(sh, &sh.n2, key, [&](int r) { return key[r] > -INFINITY; }, id_of, lane);
             __syncthreads();
-            const int c = wave_topk(key, [&](int r) { return base[r / 8] + (uint32_t)(r % 8); }, K,
-                                    sh_key + wave * FA_BEAM_MAX, sh_id + wave * FA_BEAM_MAX, lane);
-            if (lane == 0) sh_cnt[wave] = c;
+            n = sh.n2;
+            if (n <= kPickThreads) {
+                rank_candidates(sh, n, K);
+                __syncthreads();
+                n = min(n, K);
+            } else {
+                n = rank_by_rounds(sh, key, id_of, K, lane, wave);
+            }
         }
-        n = block_rank(sh_key, sh_id, sh_cnt, K, sel_key, sel_id);
         const bool bad = sh_bad != 0;
         if (tid == 0) {
             const int st = bad ? FA_ROW_BADPROB : (n == 0 ? FA_ROW_INFEASIBLE : 0);
@@ -419,10 +555,10 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
         uint32_t *to = a.states + o * W;
         for (int w = lane; w < W; w += kWave) to[w] = 0u;
         const bool live = j < n;
-        const int k = live ? (int)(sel_id[j] / (uint32_t)d.V) : j % Kin;
-        const int v = live ? (int)(sel_id[j] % (uint32_t)d.V) : -1;
+        const int k = live ? (int)(sh.sel_id[j] / (uint32_t)d.V) : j % Kin;
+        const int v = live ? (int)(sh.sel_id[j] % (uint32_t)d.V) : -1;
         if (lane == 0) {
-            a.scores[o] = live ? (float)sel_key[j] : -INFINITY;
+            a.scores[o] = live ? (float)sh.sel_key[j] : -INFINITY;
             a.tokens[o] = v;
             a.parents[o] = k;
         }
@@ -430,7 +566,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
     __syncthreads();
     for (int j = wave; j < n; j += kPickWaves) {
         uint32_t *to = a.states + ((size_t)b * K + j) * W;
-        const int k = (int)(sel_id[j] / (uint32_t)d.V), v = (int)(sel_id[j] % (uint32_t)d.V);
+        const int k = (int)(sh.sel_id[j] / (uint32_t)d.V), v = (int)(sh.sel_id[j] % (uint32_t)d.V);
         each_state(set_of(a, row0 + k, W), W, lane, [&](int s) {
             auto add = [&](int t) {
                 if (!a.reach || has_bit(a.reach, t)) atomicOr(&to[t >> 5], 1u << (t & 31));
@@ -499,48 +635,49 @@ __global__ __launch_bounds__(256) void beam_start(DevTable d, int64_t rows, int 
     }
 }
 
+struct ScanOut {
+    float *gmax;
+    double2 *part;
+    uint32_t *gmask;
+};
+
 template <class T, int MODE, int NG>
-int scan(const DevTable &d, const BeamSelect &a, float *gmax, double2 *part, hipStream_t st)
+int scan(const DevTable &d, const BeamSelect &a, const ScanOut &o, hipStream_t st)
 {
     const int64_t waves = (beam_grans(d.V) + NG - 1) / NG;
     const int64_t nblk = (waves + kScanWaves - 1) / kScanWaves;
     const int64_t blocks = nblk * a.B * a.Kin;
     if (blocks > 0x7fffffff) return -1;
-    beam_scan<T, MODE, NG><<<(unsigned)blocks, kScanWaves * kWave, 0, st>>>(d, a, gmax, part, (int)nblk);
+    beam_scan<T, MODE, NG><<<(unsigned)blocks, kScanWaves * kWave, 0, st>>>(d, a, o.gmax, o.part,
+                                                                            o.gmask, (int)nblk);
     return (int)hipGetLastError();
 }
 
-template <class T, int MODE, int RG, int RT>
-int pick(const DevTable &d, const BeamSelect &a, const float *gmax, const double2 *part, int chunks,
-         hipStream_t st)
+template <int MODE, int RG, int RT>
+int pick(const DevTable &d, const BeamSelect &a, const ScanOut &o, int chunks, hipStream_t st)
 {
-    beam_pick<T, MODE, RG, RT><<<a.B, kPickThreads, 0, st>>>(d, a, gmax, part, chunks);
+    beam_pick<MODE, RG, RT><<<a.B, kPickThreads, 0, st>>>(d, a, o.gmax, o.part, o.gmask, chunks);
     return (int)hipGetLastError();
 }
 
-template <class T, int MODE, int RG>
-int pick_tokens(const DevTable &d, const BeamSelect &a, const float *gmax, const double2 *part,
-                int chunks, hipStream_t st)
+template <int MODE, int RG>
+int pick_tokens(const DevTable &d, const BeamSelect &a, const ScanOut &o, int chunks, hipStream_t st)
 {
-    if (a.K <= kPickWaves) return pick<T, MODE, RG, 1>(d, a, gmax, part, chunks, st);
-    return pick<T, MODE, RG, 4>(d, a, gmax, part, chunks, st);
+    if (a.K <= kPickWaves) return pick<MODE, RG, 1>(d, a, o, chunks, st);
+    return pick<MODE, RG, FA_BEAM_MAX / kPickWaves>(d, a, o, chunks, st);
 }
 
-template <class T, int MODE>
-int select(const DevTable &d, const BeamSelect &a, float *gmax, double2 *part, hipStream_t st)
+template <int MODE>
+int select(const DevTable &d, const BeamSelect &a, const ScanOut &o, hipStream_t st)
 {
     constexpr int NG = 4;
-    if (int e = scan<T, MODE, NG>(d, a, gmax, part, st)) return e;
     const int nG = beam_grans(d.V), chunks = (nG + NG - 1) / NG;
-    if (a.Kin * nG <= 4 * kPickThreads) return pick_tokens<T, MODE, 4>(d, a, gmax, part, chunks, st);
-    return pick_tokens<T, MODE, 32>(d, a, gmax, part, chunks, st);
-}
-
-template <class T>
-int select_mode(const DevTable &d, const BeamSelect &a, float *gmax, double2 *part, hipStream_t st)
-{
-    return a.mode == FA_BEAM_LOGITS ? select<T, FA_BEAM_LOGITS>(d, a, gmax, part, st)
-                                    : select<T, FA_BEAM_PROBS>(d, a, gmax, part, st);
+    const int e = a.dtype == FA_F32   ? scan<float, MODE, NG>(d, a, o, st)
+                  : a.dtype == FA_F16 ? scan<_Float16, MODE, NG>(d, a, o, st)
+                                      : scan<Bf16, MODE, NG>(d, a, o, st);
+    if (e) return e;
+    if (a.Kin * nG <= 8 * kPickThreads) return pick_tokens<MODE, 8>(d, a, o, chunks, st);
+    return pick_tokens<MODE, kBeamGranMax / kPickThreads>(d, a, o, chunks, st);
 }
 
 }  // namespace
@@ -552,7 +689,8 @@ BeamWs beam_ws_layout(const HostTable &t, int32_t B, int32_t Kin)
     BeamWs w;
     w.gmax = 0;
     w.part = al(n * sizeof(float));
-    w.total = al(w.part + n * 2 * sizeof(double));
+    w.gmask = al(w.part + n * 2 * sizeof(double));
+    w.total = al(w.gmask + n * kMaskWords * sizeof(uint32_t));
     return w;
 }
 
@@ -574,12 +712,11 @@ int launch_beam_start(const DevTable &d, int B, int K, float *scores, uint32_t *
 int launch_beam_select(const DevTable &d, const BeamSelect &a, uint8_t *ws, const BeamWs &w,
                        void *stream)
 {
-    float *gmax = reinterpret_cast<float *>(ws + w.gmax);
-    double2 *part = reinterpret_cast<double2 *>(ws + w.part);
+    const ScanOut o{reinterpret_cast<float *>(ws + w.gmax), reinterpret_cast<double2 *>(ws + w.part),
+                    reinterpret_cast<uint32_t *>(ws + w.gmask)};
     hipStream_t st = (hipStream_t)stream;
-    if (a.dtype == FA_F32) return select_mode<float>(d, a, gmax, part, st);
-    if (a.dtype == FA_F16) return select_mode<_Float16>(d, a, gmax, part, st);
-    return select_mode<Bf16>(d, a, gmax, part, st);
+    return a.mode == FA_BEAM_LOGITS ? select<FA_BEAM_LOGITS>(d, a, o, st)
+                                    : select<FA_BEAM_PROBS>(d, a, o, st);
 }
 
 }  // namespace fa

@@ -404,6 +404,7 @@ struct BeamSelect {
 struct BeamWs {
     size_t gmax = 0;   // [B*Kin][granules] fp32: largest allowed value of each granule
     size_t part = 0;   // [B*Kin][granules] (maximum, sum of exp) of each wavefront's tokens
+    size_t gmask = 0;  // [B*Kin][granules][16] allowed bits of the granules that have a maximum
     size_t total = 0;
 };
 BeamWs beam_ws_layout(const HostTable &t, int32_t B, int32_t Kin);
