@@ -45,74 +45,195 @@ __device__ inline void load8(const T *row, int v, int V, float (&x)[8])
     }
 }
 
-// calls fn(state) for every state of the set, one after the other, the whole
-// wavefront at once
+// Wavefront reductions in the vector ALUs' own lane moves (within rows of 16
+// lanes, then from row to row); the result is every lane's.
+template <int CTRL, int ROWS>
+__device__ inline uint32_t lane_move(uint32_t old, uint32_t x)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, CTRL, ROWS, 0xf, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ inline double lane_move_d(double old, double x)
+{
+    const uint64_t o = (uint64_t)__double_as_longlong(old), v = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = lane_move<CTRL, ROWS>((uint32_t)o, (uint32_t)v);
+    const uint32_t hi = lane_move<CTRL, ROWS>((uint32_t)(o >> 32), (uint32_t)(v >> 32));
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
+template <class Op>
+__device__ inline float reduce_f(float x, Op op)  // op(x, x) = x
+{
+    auto mv = [](uint32_t y) { return __uint_as_float(y); };
+    x = op(x, mv(lane_move<0x111, 0xf>(__float_as_uint(x), __float_as_uint(x))));
+    x = op(x, mv(lane_move<0x112, 0xf>(__float_as_uint(x), __float_as_uint(x))));
+    x = op(x, mv(lane_move<0x114, 0xf>(__float_as_uint(x), __float_as_uint(x))));
+    x = op(x, mv(lane_move<0x118, 0xf>(__float_as_uint(x), __float_as_uint(x))));
+    x = op(x, mv(lane_move<0x142, 0xa>(__float_as_uint(x), __float_as_uint(x))));
+    x = op(x, mv(lane_move<0x143, 0xc>(__float_as_uint(x), __float_as_uint(x))));
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+}
+
+__device__ inline double last_lane_d(double x)
+{
+    const uint64_t v = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, 63);
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), 63);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
+__device__ inline double reduce_max_d(double x)
+{
+    x = fmax(x, lane_move_d<0x111, 0xf>(x, x));
+    x = fmax(x, lane_move_d<0x112, 0xf>(x, x));
+    x = fmax(x, lane_move_d<0x114, 0xf>(x, x));
+    x = fmax(x, lane_move_d<0x118, 0xf>(x, x));
+    x = fmax(x, lane_move_d<0x142, 0xa>(x, x));
+    x = fmax(x, lane_move_d<0x143, 0xc>(x, x));
+    return last_lane_d(x);
+}
+
+__device__ inline double reduce_sum_d(double x)
+{
+    x += lane_move_d<0x111, 0xf>(0.0, x);
+    x += lane_move_d<0x112, 0xf>(0.0, x);
+    x += lane_move_d<0x114, 0xf>(0.0, x);
+    x += lane_move_d<0x118, 0xf>(0.0, x);
+    x += lane_move_d<0x142, 0xa>(0.0, x);
+    x += lane_move_d<0x143, 0xc>(0.0, x);
+    return last_lane_d(x);
+}
+
+__device__ inline int scan_sum_i(int v)  // inclusive
+{
+    uint32_t x = (uint32_t)v;
+    x += lane_move<0x111, 0xf>(0u, x);
+    x += lane_move<0x112, 0xf>(0u, x);
+    x += lane_move<0x114, 0xf>(0u, x);
+    x += lane_move<0x118, 0xf>(0u, x);
+    x += lane_move<0x142, 0xa>(0u, x);
+    x += lane_move<0x143, 0xc>(0u, x);
+    return (int)x;
+}
+
+// A state set's members, up to 64 at a time, one a lane: calls fn(state, n)
+// with lanes 0 .. n-1 holding a state each.  `list` is 64 LDS words of the
+// wavefront's own.
 template <class Fn>
-__device__ inline void each_state(const uint32_t *set, int W, int lane, Fn fn)
+__device__ inline void each_states(const uint32_t *set, int W, uint32_t *list, int lane, Fn fn)
 {
     for (int w0 = 0; w0 < W; w0 += kWave) {
         const uint32_t word = w0 + lane < W ? set[w0 + lane] : 0u;
-        unsigned long long nz = __ballot(word != 0u);
-        while (nz) {
-            const int l = __ffsll(nz) - 1;
-            nz &= nz - 1;
-            uint32_t bits = __builtin_amdgcn_readlane(word, l);
-            while (bits) {
-                fn((w0 + l) * 32 + __ffs(bits) - 1);
-                bits &= bits - 1;
-            }
+        if (!__ballot(word != 0u)) continue;
+        const int own = __popc(word), upto = scan_sum_i(own);
+        const int total = __builtin_amdgcn_readlane(upto, 63);
+        for (int from = 0; from < total; from += kWave) {
+            int at = upto - own - from;
+            for (uint32_t bits = word; bits; bits &= bits - 1, ++at)
+                if (at >= 0 && at < kWave) list[at] = (uint32_t)((w0 + lane) * 32 + __ffs(bits) - 1);
+            wave_sync();
+            const int n = min(total - from, kWave);
+            const int s = lane < n ? (int)list[lane] : 0;
+            wave_sync();
+            fn(s, n);
         }
     }
 }
 
+// Items [lo, hi) of every lane's own, taken 64 at a time by all lanes:
+// fn(item), -1 where a lane has none left.
+template <class Fn>
+__device__ inline void each_item(int lo, int hi, int n, int lane, Fn fn)
+{
+    const int cnt = hi - lo;
+    if (n == 1) {  // one owner, as on a deterministic automaton
+        const int l0 = __builtin_amdgcn_readfirstlane(lo), h0 = __builtin_amdgcn_readfirstlane(hi);
+        for (int i = l0; i < h0; i += kWave) fn(i + lane < h0 ? i + lane : -1);
+        return;
+    }
+    const int upto = scan_sum_i(cnt);
+    const int total = __builtin_amdgcn_readlane(upto, 63);
+    for (int i0 = 0; i0 < total; i0 += kWave) {
+        const int i = i0 + lane;
+        int own = 0;  // lanes whose items all come before
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1)
+            if (__shfl(upto, own + o - 1) <= i) own += o;
+        own = min(own, kWave - 1);
+        const int at = i - (__shfl(upto, own) - __shfl(cnt, own));
+        const int first = __shfl(lo, own);
+        fn(i < total ? first + at : -1);
+    }
+}
+
+constexpr int kListWords = kWave;
+
 // mask[0 .. ng*16): bit t set when token g0*512 + t may follow the state set.
-// The wavefront's own LDS words.
+// mask and list are the wavefront's own LDS words.
 __device__ inline void allowed_mask(const DevTable &d, const uint32_t *set, int W,
-                                    const uint32_t *reach, int g0, int ng, uint32_t *mask, int lane)
+                                    const uint32_t *reach, int g0, int ng, uint32_t *mask,
+                                    uint32_t *list, int lane)
 {
     const int words = ng * kMaskWords, t0 = g0 * kBeamGran, t1 = t0 + ng * kBeamGran;
     const int nG = beam_grans(d.V);
     for (int w = lane; w < words; w += kWave) mask[w] = 0u;
     wave_sync();
-    each_state(set, W, lane, [&](int s) {
+    each_states(set, W, list, lane, [&](int s, int n) {
+        const bool mine = lane < n;
         const int32_t *off = d.bm_off + (size_t)s * (nG + 1);
-        const int e1 = off[min(g0 + ng, nG)];
-        for (int e = off[g0] + lane; e < e1; e += kWave) {
-            const int tok = d.bm_ent[2 * (size_t)e], to = d.bm_ent[2 * (size_t)e + 1];
-            if (!reach || has_bit(reach, to)) atomicOr(&mask[(tok - t0) >> 5], 1u << (tok & 31));
-        }
-        for (int i = d.bm_doff[s]; i < d.bm_doff[s + 1]; ++i) {
-            const int j = d.bm_dense[2 * (size_t)i], to = d.bm_dense[2 * (size_t)i + 1];
-            if (reach && !has_bit(reach, to)) continue;
-            const uint32_t *bits = d.dense_bits + (size_t)j * d.dense_words;
-            for (int w = lane; w < words; w += kWave) {
-                const int gw = t0 / 32 + w;
-                if (gw < d.dense_words) atomicOr(&mask[w], bits[gw]);
-            }
-        }
-        // range labels: 64 segments a time, those that meet the tokens one by one
-        const int s1 = d.bm_soff[s + 1];
-        for (int i0 = d.bm_soff[s]; i0 < s1; i0 += kWave) {
-            int lo = 0, hi = 0;
-            if (i0 + lane < s1) {
-                const int32_t *sg = d.bm_seg + 4 * (size_t)(i0 + lane);
-                if (!reach || has_bit(reach, sg[2])) {
-                    lo = max(sg[0], t0);
-                    hi = min(sg[1], t1);
+        const int e0 = mine ? off[g0] : 0, e1 = mine ? off[min(g0 + ng, nG)] : 0;
+        const int d0 = mine ? d.bm_doff[s] : 0, d1 = mine ? d.bm_doff[s + 1] : 0;
+        const int s0 = mine ? d.bm_soff[s] : 0, s1 = mine ? d.bm_soff[s + 1] : 0;
+        each_item(e0, e1, n, lane, [&](int e) {
+            if (e < 0) return;
+            const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
+            if (!reach || has_bit(reach, en.y)) atomicOr(&mask[(en.x - t0) >> 5], 1u << (en.x & 31));
+        });
+        if (__ballot(d1 > d0)) {
+            each_item(d0, d1, n, lane, [&](int i) {
+                int j = -1;
+                if (i >= 0) {
+                    const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
+                    if (!reach || has_bit(reach, dn.y)) j = dn.x;
                 }
-            }
-            unsigned long long hit = __ballot(lo < hi);
-            while (hit) {
-                const int l = __ffsll(hit) - 1;
-                hit &= hit - 1;
-                const int a = __builtin_amdgcn_readlane(lo, l) - t0;
-                const int b = __builtin_amdgcn_readlane(hi, l) - t0;
-                for (int w = (a >> 5) + lane; w <= (b - 1) >> 5; w += kWave) {
-                    const uint32_t from = a > 32 * w ? ~0u << (a - 32 * w) : ~0u;
-                    const uint32_t upto = b < 32 * w + 32 ? ~(~0u << (b - 32 * w)) : ~0u;
-                    atomicOr(&mask[w], from & upto);
+                unsigned long long hit = __ballot(j >= 0);
+                while (hit) {
+                    const int l = __ffsll(hit) - 1;
+                    hit &= hit - 1;
+                    const uint32_t *bits =
+                        d.dense_bits + (size_t)__builtin_amdgcn_readlane(j, l) * d.dense_words;
+                    for (int w = lane; w < words; w += kWave) {
+                        const int gw = t0 / 32 + w;
+                        if (gw < d.dense_words) atomicOr(&mask[w], bits[gw]);
+                    }
                 }
-            }
+            });
+        }
+        if (__ballot(s1 > s0)) {
+            // range labels: those that meet the tokens, one by one
+            each_item(s0, s1, n, lane, [&](int i) {
+                int lo = 0, hi = 0;
+                if (i >= 0) {
+                    const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
+                    if (!reach || has_bit(reach, sg.z)) {
+                        lo = max(sg.x, t0);
+                        hi = min(sg.y, t1);
+                    }
+                }
+                unsigned long long hit = __ballot(lo < hi);
+                while (hit) {
+                    const int l = __ffsll(hit) - 1;
+                    hit &= hit - 1;
+                    const int a = __builtin_amdgcn_readlane(lo, l) - t0;
+                    const int b = __builtin_amdgcn_readlane(hi, l) - t0;
+                    for (int w = (a >> 5) + lane; w <= (b - 1) >> 5; w += kWave) {
+                        const uint32_t from = a > 32 * w ? ~0u << (a - 32 * w) : ~0u;
+                        const uint32_t upto = b < 32 * w + 32 ? ~(~0u << (b - 32 * w)) : ~0u;
+                        atomicOr(&mask[w], from & upto);
+                    }
+                }
+            });
         }
     });
     wave_sync();
@@ -162,7 +283,7 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
                                                                double2 *__restrict__ part,
                                                                uint32_t *__restrict__ gmask, int nblk)
 {
-    __shared__ uint32_t sh_mask[kScanWaves][NG * kMaskWords];
+    __shared__ uint32_t sh_mask[kScanWaves][NG * kMaskWords + kListWords];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = blockIdx.x / nblk;
     const int chunk = (blockIdx.x % nblk) * kScanWaves + wave;
@@ -175,7 +296,7 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
 #pragma unroll
     for (int i = 0; i < NG; ++i) load8(x, min((g0 + i) * kBeamGran + lane * 8, d.V), d.V, v[i]);
     uint32_t *mask = sh_mask[wave];
-    allowed_mask(d, set_of(a, row, W), W, a.reach, g0, NG, mask, lane);
+    allowed_mask(d, set_of(a, row, W), W, a.reach, g0, NG, mask, mask + NG * kMaskWords, lane);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
@@ -191,7 +312,7 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
                 best = fmaxf(best, y);
                 if (MODE == FA_BEAM_PROBS) bad |= on && !(y >= 0.f && y < INFINITY);
             }
-            best = wave_max_f(best);
+            best = reduce_f(best, [](float p, float q) { return fmaxf(p, q); });
             // a bad probability travels as a NaN maximum
             if (MODE == FA_BEAM_PROBS && __ballot(bad)) best = NAN;
             // for the second kernel, should the granule be among the best
@@ -205,8 +326,7 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
         }
     }
     if (MODE == FA_BEAM_LOGITS) {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, o));
+        m = reduce_f(m, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
         double s = m;  // NaN or +inf: the row is flagged
         if (m == -INFINITY) s = 0.0;
         else if (m < INFINITY) {
@@ -218,7 +338,7 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
                 for (int j = 0; j < 8; ++j)
                     // the difference first: it is exact, whatever the size of the logits
                     s += exp2_poly(fmax(((double)v[i][j] - (double)m) * kLog2e, -1100.0));
-            s = wave_sum_d(s);
+            s = reduce_sum_d(s);
         }
         if (lane == 0) part[(size_t)row * nG + chunk] = make_double2((double)m, s);
     }
@@ -227,13 +347,6 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
 __device__ inline bool before(double k0, uint32_t i0, double k1, uint32_t i1)
 {
     return k0 > k1 || (k0 == k1 && i0 < i1);
-}
-
-__device__ inline double wave_max_d(double x)
-{
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x = fmax(x, __shfl_xor(x, o));
-    return x;
 }
 
 // The first K of the wavefront's R keys a lane (order: `before`; -inf is no
@@ -256,7 +369,7 @@ __device__ inline int wave_topk(double (&key)[R], Id id_of, int K, double *out_k
                 br = r;
             }
         }
-        const double best = wave_max_d(bk);
+        const double best = reduce_max_d(bk);
         if (best == -INFINITY) break;
         uint32_t low = bk == best ? bi : ~0u;
 #pragma unroll
@@ -297,24 +410,38 @@ struct PickShared {
     uint32_t sel_id[FA_BEAM_MAX];
     int cnt[kPickWaves];
     uint32_t tau[2][kPickWaves];
+    int rank[kPickThreads];
     int n;  // candidates found, in either round
     int n2;
 };
 
-// The candidates, unordered, in key / id: each ranked against all of them;
-// those below K go to their rank in sel_key / sel_id.
+// The n candidates, unordered, in key / id: each ranked against all of them,
+// the comparisons spread over all threads; those below K go to their rank in
+// sel_key / sel_id.  rank is zero before and after.  The workgroup comes in
+// and leaves in step.
 __device__ inline void rank_candidates(PickShared &sh, int n, int K)
 {
-    if ((int)threadIdx.x < n) {
-        const double mk = sh.key[threadIdx.x];
-        const uint32_t mi = sh.id[threadIdx.x];
+    const int tid = threadIdx.x;
+    const int lg = n > 1 ? 32 - __clz(n - 1) : 0;
+    const int i = tid & ((1 << lg) - 1), parts = kPickThreads >> lg;
+    if (i < n) {
+        const double mk = sh.key[i];
+        const uint32_t mi = sh.id[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += before(sh.key[j], sh.id[j], mk, mi);
+#pragma unroll 4
+        for (int j = tid >> lg; j < n; j += parts) rank += before(sh.key[j], sh.id[j], mk, mi);
+        atomicAdd(&sh.rank[i], rank);
+    }
+    __syncthreads();
+    if (tid < n) {
+        const int rank = sh.rank[tid];
+        sh.rank[tid] = 0;
         if (rank < K) {
-            sh.sel_key[rank] = mk;
-            sh.sel_id[rank] = mi;
+            sh.sel_key[rank] = sh.key[tid];
+            sh.sel_id[rank] = sh.id[tid];
         }
     }
+    __syncthreads();
 }
 
 // Where more candidates tie than the list holds: the wavefronts' own first K
@@ -402,11 +529,13 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
     __shared__ double sh_lse[FA_BEAM_MAX];
     __shared__ double sh_score[FA_BEAM_MAX];
     __shared__ PickShared sh;
+    __shared__ uint32_t sh_list[kPickWaves][kListWords];
     __shared__ int sh_bad;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int nG = beam_grans(d.V), W = (d.S + 31) / 32, Kin = a.Kin, K = a.K;
     const int row0 = b * Kin, M = Kin * nG;
     const bool flagged = a.status[b] != 0;
+    sh.rank[tid] = 0;
     if (tid == 0) {
         sh_bad = 0;
         sh.n = 0;
@@ -425,21 +554,28 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
             const float sc = a.scores_in[row0 + k];
             double lse = MODE == FA_BEAM_LOGITS ? -INFINITY : 0.0;
             bool bad = !(sc < INFINITY);
-            if (MODE == FA_BEAM_LOGITS && sc > -INFINITY && !bad) {
-                double m = -INFINITY, s = 0.0;
+            if (MODE == FA_BEAM_LOGITS) {
+                // asked for before the score is known: an empty slot's are not used
                 const double2 *pr = part + (size_t)(row0 + k) * nG;
-                bool odd = false;
-                for (int c = lane; c < chunks; c += kWave) {
-                    m = fmax(m, pr[c].x);
-                    odd |= !(pr[c].x < INFINITY);
+                const double2 none = make_double2(-INFINITY, 0.0);
+                const double2 p0 = lane < chunks ? pr[lane] : none;
+                const double2 p1 = lane + kWave < chunks ? pr[lane + kWave] : none;
+                if (sc > -INFINITY && !bad) {
+                    double m = fmax(p0.x, p1.x), s = 0.0;
+                    bool odd = !(p0.x < INFINITY) || !(p1.x < INFINITY);
+                    for (int c = lane + 2 * kWave; c < chunks; c += kWave) {
+                        m = fmax(m, pr[c].x);
+                        odd |= !(pr[c].x < INFINITY);
+                    }
+                    bad = __ballot(odd) != 0ull;
+                    m = reduce_max_d(m);
+                    if (!bad && m > -INFINITY) {
+                        auto term = [&](double2 p) { return p.x > -INFINITY ? p.y * exp(p.x - m) : 0.0; };
+                        s = term(p0) + term(p1);
+                        for (int c = lane + 2 * kWave; c < chunks; c += kWave) s += term(pr[c]);
+                        lse = m + log(reduce_sum_d(s));
+                    }
                 }
-                m = wave_max_d(m);
-                for (int c = lane; c < chunks; c += kWave)
-                    if (pr[c].x > -INFINITY) s += pr[c].y * exp(pr[c].x - m);
-                s = wave_sum_d(s);
-                if (m > -INFINITY) lse = m + log(s);
-                bad = __ballot(odd) != 0ull;
-                if (bad) lse = -INFINITY;
             }
             if (lane == 0) {
                 sh_lse[k] = lse;
@@ -494,7 +630,6 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
             ng = sh.n;
             if (ng <= kPickThreads) {
                 rank_candidates(sh, ng, K);
-                __syncthreads();
                 ng = min(ng, K);
             } else {
                 ng = rank_by_rounds(sh, key, id_of, K, lane, wave);
@@ -536,7 +671,6 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
             n = sh.n2;
             if (n <= kPickThreads) {
                 rank_candidates(sh, n, K);
-                __syncthreads();
                 n = min(n, K);
             } else {
                 n = rank_by_rounds(sh, key, id_of, K, lane, wave);
@@ -567,20 +701,32 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
     for (int j = wave; j < n; j += kPickWaves) {
         uint32_t *to = a.states + ((size_t)b * K + j) * W;
         const int k = (int)(sh.sel_id[j] / (uint32_t)d.V), v = (int)(sh.sel_id[j] % (uint32_t)d.V);
-        each_state(set_of(a, row0 + k, W), W, lane, [&](int s) {
+        each_states(set_of(a, row0 + k, W), W, sh_list[wave], lane, [&](int s, int m) {
             auto add = [&](int t) {
                 if (!a.reach || has_bit(a.reach, t)) atomicOr(&to[t >> 5], 1u << (t & 31));
             };
+            const bool mine = lane < m;
             const int32_t *off = d.bm_off + (size_t)s * (nG + 1) + v / kBeamGran;
-            for (int e = off[0] + lane; e < off[1]; e += kWave)
-                if (d.bm_ent[2 * (size_t)e] == v) add(d.bm_ent[2 * (size_t)e + 1]);
-            for (int i = d.bm_doff[s] + lane; i < d.bm_doff[s + 1]; i += kWave)
-                if (has_bit(d.dense_bits + (size_t)d.bm_dense[2 * (size_t)i] * d.dense_words, v))
-                    add(d.bm_dense[2 * (size_t)i + 1]);
-            for (int i = d.bm_soff[s] + lane; i < d.bm_soff[s + 1]; i += kWave) {
-                const int32_t *sg = d.bm_seg + 4 * (size_t)i;
-                if (sg[0] <= v && v < sg[1]) add(sg[2]);
-            }
+            const int e0 = mine ? off[0] : 0, e1 = mine ? off[1] : 0;
+            const int d0 = mine ? d.bm_doff[s] : 0, d1 = mine ? d.bm_doff[s + 1] : 0;
+            const int s0 = mine ? d.bm_soff[s] : 0, s1 = mine ? d.bm_soff[s + 1] : 0;
+            each_item(e0, e1, m, lane, [&](int e) {
+                if (e < 0) return;
+                const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
+                if (en.x == v) add(en.y);
+            });
+            if (__ballot(d1 > d0))
+                each_item(d0, d1, m, lane, [&](int i) {
+                    if (i < 0) return;
+                    const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
+                    if (has_bit(d.dense_bits + (size_t)dn.x * d.dense_words, v)) add(dn.y);
+                });
+            if (__ballot(s1 > s0))
+                each_item(s0, s1, m, lane, [&](int i) {
+                    if (i < 0) return;
+                    const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
+                    if (sg.x <= v && v < sg.y) add(sg.z);
+                });
         });
     }
 }
@@ -653,6 +799,14 @@ int scan(const DevTable &d, const BeamSelect &a, const ScanOut &o, hipStream_t s
     return (int)hipGetLastError();
 }
 
+template <class T, int MODE>
+int scan_any(const DevTable &d, const BeamSelect &a, const ScanOut &o, int NG, hipStream_t st)
+{
+    if (NG == 1) return scan<T, MODE, 1>(d, a, o, st);
+    if (NG == 2) return scan<T, MODE, 2>(d, a, o, st);
+    return scan<T, MODE, 4>(d, a, o, st);
+}
+
 template <int MODE, int RG, int RT>
 int pick(const DevTable &d, const BeamSelect &a, const ScanOut &o, int chunks, hipStream_t st)
 {
@@ -670,11 +824,17 @@ int pick_tokens(const DevTable &d, const BeamSelect &a, const ScanOut &o, int ch
 template <int MODE>
 int select(const DevTable &d, const BeamSelect &a, const ScanOut &o, hipStream_t st)
 {
-    constexpr int NG = 4;
-    const int nG = beam_grans(d.V), chunks = (nG + NG - 1) / NG;
-    const int e = a.dtype == FA_F32   ? scan<float, MODE, NG>(d, a, o, st)
-                  : a.dtype == FA_F16 ? scan<_Float16, MODE, NG>(d, a, o, st)
-                                      : scan<Bf16, MODE, NG>(d, a, o, st);
+    const int nG = beam_grans(d.V);
+    // granules of a wavefront: few where the wavefronts would not fill the
+    // chip (4096 granules, us at 1 / 2 / 4: 7.8 / 8.6 / 11.0; 9504: 11.1 /
+    // 9.4 / 11.5), more where each one's fixed work counts (304,128: 230 /
+    // 177 / 163; at 8, 184)
+    const int64_t all = (int64_t)a.B * a.Kin * nG;
+    const int NG = all <= 8192 ? 1 : all <= 32768 ? 2 : 4;
+    const int chunks = (nG + NG - 1) / NG;
+    const int e = a.dtype == FA_F32   ? scan_any<float, MODE>(d, a, o, NG, st)
+                  : a.dtype == FA_F16 ? scan_any<_Float16, MODE>(d, a, o, NG, st)
+                                      : scan_any<Bf16, MODE>(d, a, o, NG, st);
     if (e) return e;
     if (a.Kin * nG <= 8 * kPickThreads) return pick_tokens<MODE, 8>(d, a, o, chunks, st);
     return pick_tokens<MODE, kBeamGranMax / kPickThreads>(d, a, o, chunks, st);
