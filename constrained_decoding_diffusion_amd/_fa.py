@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -49,6 +50,8 @@ class _BeamItem(C.Structure):
                                  "dst_batch_stride", "dst_beam_stride", "dst_row_stride", "rows",
                                  "row_bytes")]
 
+
+_BEAM_ITEM = struct.Struct("10q")  # its memory image
 
 _lib = None
 
@@ -390,20 +393,19 @@ class BeamBuffers:
             self.ws = torch.empty(n.value, dtype=torch.uint8, device=device)
 
 
-def _device_of(table: Table, t):
-    """Uploads the table where t lives if it is nowhere yet."""
-    if table.buf is None:
-        table.upload(t.device)
-    elif table.buf.device != t.device:
-        raise ValueError(f"the table is on {table.buf.device}, the input on {t.device}")
-    return t.device
-
-
-def _on(device):
-    """The device made current (HIP launches go to the current device), and
-    torch's current stream of it."""
+def _launch(fn: str, device, *args):
+    """The library call fn(*args, stream) on torch's current stream of the
+    device, made current if it is not (HIP launches go to the current device)."""
     import torch
-    return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    f = getattr(_lib, fn)
+    i = device.index
+    if torch.cuda.current_device() == i:
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if rc != FA_OK:
+        raise FaError(fn, rc)
 
 
 def beam_lookahead(table: Table, L: int, device="cuda"):
@@ -415,10 +417,7 @@ def beam_lookahead(table: Table, L: int, device="cuda"):
         table.upload(device)
     sets = torch.empty((max(L, 0) + 1, (table.info["S"] + 31) // 32), dtype=torch.int32,
                        device=table.buf.device)
-    guard, stream = _on(sets.device)
-    with guard:
-        _check("fa_beam_lookahead", lib().fa_beam_lookahead(table.handle, L, _ptr(sets),
-                                                            C.c_void_p(stream)))
+    _launch("fa_beam_lookahead", sets.device, table.handle, L, sets.data_ptr())
     return sets
 
 
@@ -428,10 +427,8 @@ def beam_start(table: Table, B: int, K: int, device="cuda"):
     if table.buf is None:
         table.upload(device)
     beams = BeamBuffers(table, B, K, device=table.buf.device)
-    guard, stream = _on(table.buf.device)
-    with guard:
-        _check("fa_beam_start", lib().fa_beam_start(table.handle, B, K, _ptr(beams.scores),
-                                                    _ptr(beams.states), C.c_void_p(stream)))
+    _launch("fa_beam_start", table.buf.device, table.handle, B, K, beams.scores.data_ptr(),
+            beams.states.data_ptr())
     return beams
 
 
@@ -454,7 +451,7 @@ def beam_select(table: Table, logits, beams: BeamBuffers, out: BeamBuffers = Non
     come, this one included; without one a hypothesis may run into a dead end.
     Returns out (a new BeamBuffers of beams.K slots by default; not beams
     itself), whose status is that of beams."""
-    if logits.dim() != 3 or tuple(logits.shape) != (beams.B, beams.K, table.info["V"]):
+    if logits.dim() != 3 or logits.shape != (beams.B, beams.K, table.info["V"]):
         raise ValueError(f"logits has shape {tuple(logits.shape)}, expected "
                          f"{(beams.B, beams.K, table.info['V'])}")
     dtype = _beam_dtype(logits)
@@ -462,29 +459,32 @@ def beam_select(table: Table, logits, beams: BeamBuffers, out: BeamBuffers = Non
     sb, sk, sv = logits.stride()
     if not logits.is_cuda or (V > 1 and sv != 1):
         raise ValueError("logits must be a cuda tensor, contiguous in its last dimension")
-    dev = _device_of(table, logits)
+    dev = logits.device
+    if table.buf is None:
+        table.upload(dev)
     if out is None:
         out = BeamBuffers(table, B, Kin, like=beams)
     elif out is beams or out.B != B or out.words != beams.words:
         raise ValueError("out must be other buffers of the same batch and table")
-    for t in (beams.scores, out.scores) + (() if lookahead is None else (lookahead,)):
-        if t.device != dev:
-            raise ValueError(f"the beams and the lookahead must be on {dev}")
+    if table.buf.device != dev or beams.scores.device != dev or out.scores.device != dev:
+        raise ValueError(f"the table and the beams must be on {dev}")
     if lookahead is None:
         if steps_left != 0:
             raise ValueError("steps_left needs a lookahead")
-    elif (lookahead.dim() != 2 or lookahead.shape[1] != beams.words or not lookahead.is_contiguous()
-          or lookahead.element_size() != 4):
-        raise ValueError("lookahead must come from beam_lookahead of this table")
-    elif not 1 <= steps_left < lookahead.shape[0]:
-        raise ValueError(f"steps_left is {steps_left}, the lookahead covers 1..{lookahead.shape[0] - 1}")
-    guard, stream = _on(dev)
-    with guard:
-        _check("fa_beam_select", lib().fa_beam_select(
-            table.handle, dtype, _ptr(logits), sb if B > 1 else 0, sk if Kin > 1 else 0, B, Kin,
-            out.K, mode, _ptr(beams.scores), _ptr(beams.states), _ptr(lookahead), steps_left,
-            _ptr(out.scores), _ptr(out.tokens), _ptr(out.parents), _ptr(out.states),
-            _ptr(beams.ws), beams.ws.numel(), _ptr(beams.status), C.c_void_p(stream)))
+        ahead = None
+    else:
+        if (lookahead.device != dev or lookahead.dim() != 2 or lookahead.shape[1] != beams.words
+                or not lookahead.is_contiguous() or lookahead.element_size() != 4):
+            raise ValueError(f"lookahead must come from beam_lookahead of this table, on {dev}")
+        if not 1 <= steps_left < lookahead.shape[0]:
+            raise ValueError(f"steps_left is {steps_left}, the lookahead covers "
+                             f"1..{lookahead.shape[0] - 1}")
+        ahead = lookahead.data_ptr()
+    _launch("fa_beam_select", dev, table.handle, dtype, logits.data_ptr(), sb if B > 1 else 0,
+            sk if Kin > 1 else 0, B, Kin, out.K, mode, beams.scores.data_ptr(),
+            beams.states.data_ptr(), ahead, steps_left, out.scores.data_ptr(),
+            out.tokens.data_ptr(), out.parents.data_ptr(), out.states.data_ptr(),
+            beams.ws.data_ptr(), beams.ws.numel(), beams.status.data_ptr())
     out.status = beams.status
     return out
 
@@ -510,6 +510,24 @@ def _slot_rows(t):
     return n, stride, row
 
 
+def _move_layout(s, d):
+    """The fields of a _BeamItem behind its pointers: strides of source and
+    destination, rows, row bytes, both slots cut into the same pieces."""
+    rows, sr, row = _slot_rows(s)
+    rows_d, dr, row_d = _slot_rows(d)
+    if row != row_d and rows * row:
+        # one of them is contiguous over more dimensions
+        piece = min(row, row_d)
+        if rows == 1 and row % piece == 0:
+            rows, sr, row = row // piece, piece, piece
+        if rows_d == 1 and row_d % piece == 0:
+            rows_d, dr, row_d = row_d // piece, piece, piece
+    if (rows, row) != (rows_d, row_d):
+        raise ValueError("tensors and out cut their slots into different pieces")
+    e = s.element_size()
+    return (s.stride(0) * e, s.stride(1) * e, sr, d.stride(0) * e, d.stride(1) * e, dr, rows, row)
+
+
 def beam_reorder(tensors, parents, out=None):
     """Moves per-hypothesis memory after the chosen parents
     (fa_beam_reorder) on torch's current stream: slot (b, k) of every tensor
@@ -523,37 +541,24 @@ def beam_reorder(tensors, parents, out=None):
             or not parents.is_cuda:
         raise ValueError("parents must be a contiguous cuda int32 [B, K] tensor")
     B, K = parents.shape
+    lib()
     dst = tensors if out is None else out
     if len(dst) != len(tensors):
         raise ValueError("out must hold one tensor for each of tensors")
     items = (_BeamItem * max(len(tensors), 1))()
-    for it, s, d in zip(items, tensors, dst):
-        if s.dim() < 2 or tuple(s.shape[:2]) != (B, K) or s.shape != d.shape or s.dtype != d.dtype:
-            raise ValueError(f"expected [{B}, {K}, ...] tensors, and out of the same shapes and types")
-        if s.device != parents.device or d.device != parents.device:
-            raise ValueError(f"every tensor must be on {parents.device}")
-        rows, sr, row = _slot_rows(s)
-        rows_d, dr, row_d = (rows, sr, row) if d is s else _slot_rows(d)
-        # the common pieces of both layouts
-        piece = min(row, row_d)
-        if (rows, row) != (rows_d, row_d):
-            if piece == 0 or row % piece or row_d % piece:
-                raise ValueError("tensors and out cut their slots into different pieces")
-            if rows == 1:
-                rows, sr, row = row // piece, piece, piece
-            if rows_d == 1:
-                rows_d, dr, row_d = row_d // piece, piece, piece
-            if (rows, row) != (rows_d, row_d):
-                raise ValueError("tensors and out cut their slots into different pieces")
-        e = s.element_size()
-        it.src, it.dst = s.data_ptr(), d.data_ptr()
-        it.src_batch_stride, it.src_beam_stride, it.src_row_stride = s.stride(0) * e, s.stride(1) * e, sr
-        it.dst_batch_stride, it.dst_beam_stride, it.dst_row_stride = d.stride(0) * e, d.stride(1) * e, dr
-        it.rows, it.row_bytes = rows, row
-    guard, stream = _on(parents.device)
-    with guard:
-        _check("fa_beam_reorder", lib().fa_beam_reorder(items, len(tensors), B, K, _ptr(parents),
-                                                        C.c_void_p(stream)))
+    dev = parents.device
+    last = layout = None
+    for i, (s, d) in enumerate(zip(tensors, dst)):
+        key = (s.shape, s.stride(), s.dtype, s.device, d.shape, d.stride(), d.dtype, d.device)
+        if key != last:  # tensors of one layout follow each other
+            if s.dim() < 2 or s.shape[:2] != (B, K) or s.shape != d.shape or s.dtype != d.dtype:
+                raise ValueError(f"expected [{B}, {K}, ...] tensors, and out of the same shapes "
+                                 "and types")
+            if s.device != dev or d.device != dev:
+                raise ValueError(f"every tensor must be on {dev}")
+            layout, last = _move_layout(s, d), key
+        _BEAM_ITEM.pack_into(items, i * _BEAM_ITEM.size, s.data_ptr(), d.data_ptr(), *layout)
+    _launch("fa_beam_reorder", dev, items, len(tensors), B, K, parents.data_ptr())
     return dst
 
 
@@ -569,10 +574,9 @@ def beam_trace(tokens, parents):
         raise ValueError("tokens and parents must have one shape and device")
     T, B, K = tokens.shape
     res = torch.empty((B, K, T), dtype=torch.int32, device=tokens.device)
-    guard, stream = _on(tokens.device)
-    with guard:
-        _check("fa_beam_trace", lib().fa_beam_trace(T, B, K, _ptr(tokens), _ptr(parents), _ptr(res),
-                                                    C.c_void_p(stream)))
+    lib()
+    _launch("fa_beam_trace", tokens.device, T, B, K, tokens.data_ptr(), parents.data_ptr(),
+            res.data_ptr())
     return res
 
 

@@ -15,8 +15,8 @@ struct MoveItem {
     const char *src;
     char *dst;
     int64_t sb, sk, sr, db, dk, dr;  // batch, slot and row strides
-    int64_t row_bytes;
-    uint32_t per_row;  // units of a row, its last one shorter when 16 does not divide it
+    uint32_t full;     // units of 16 bytes of a row
+    uint32_t per_row;  // and the bytes behind them, a unit each
     uint32_t units;    // of a slot
     uint32_t blocks;   // workgroups of a batch row
     uint32_t first;    // first workgroup of the item
@@ -28,73 +28,56 @@ struct MoveArgs {
 };
 static_assert(sizeof(MoveArgs) <= 4096, "kernel arguments");
 
-template <class T>
-__device__ inline T load_as(const char *p)
+template <class U, int KMAX>
+__device__ __forceinline__ void move_unit(const char *src, char *dst, int64_t sk, int64_t dk,
+                                          const int (&from)[KMAX], int K, bool in_place)
 {
-    T x;
-    __builtin_memcpy(&x, p, sizeof(T));  // any alignment
-    return x;
+    U x[KMAX];
+#pragma unroll
+    for (int k = 0; k < KMAX; ++k) {
+        if (k < K && !(in_place && from[k] == k)) {
+            U y;
+            __builtin_memcpy(&y, src + from[k] * sk, sizeof(U));  // any alignment
+            x[k] = y;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < KMAX; ++k) {
+        if (k < K && !(in_place && from[k] == k)) {
+            const U y = x[k];
+            __builtin_memcpy(dst + k * dk, &y, sizeof(U));
+        }
+    }
 }
 
-// One thread: one unit of every slot of a batch row.  All slots are loaded
-// before any is stored, and no other thread touches these bytes, so the
-// permutation needs no second buffer whatever the parents are.
+// One thread: one unit of every slot of a batch row, 16 bytes or one of the
+// row's last bytes.  All slots are loaded before any is stored, and no other
+// thread touches these bytes, so the permutation needs no second buffer
+// whatever the parents are.
 template <int KMAX>
 __global__ __launch_bounds__(kMoveThreads) void beam_move(MoveArgs a)
 {
     int i = 0;
     while (i + 1 < a.n && blockIdx.x >= a.it[i + 1].first) ++i;
-    const MoveItem &m = a.it[i];
+    const MoveItem m = a.it[i];
     const uint32_t blk = blockIdx.x - m.first;
-    const int b = blk / m.blocks;
+    const int b = blk / m.blocks, K = a.K;
     const uint32_t u = (blk % m.blocks) * kMoveThreads + threadIdx.x;
     if (u >= m.units) return;
-    const uint32_t r = u / m.per_row, c = u % m.per_row;
-    const char *src = m.src + (int64_t)b * m.sb + (int64_t)r * m.sr + (int64_t)c * kUnit;
-    char *dst = m.dst + (int64_t)b * m.db + (int64_t)r * m.dr + (int64_t)c * kUnit;
-    const int left = (int)min((int64_t)kUnit, m.row_bytes - (int64_t)c * kUnit);
+    const int32_t *par = a.parents + (size_t)b * K;
+    int from[KMAX];
+#pragma unroll
+    for (int k = 0; k < KMAX; ++k) from[k] = par[min(k, K - 1)];
+#pragma unroll
+    for (int k = 0; k < KMAX; ++k)
+        if (from[k] < 0 || from[k] >= K) from[k] = k;
     const bool in_place = m.src == m.dst;
-    const int32_t *par = a.parents + (size_t)b * a.K;
-    uint4 x[KMAX];
-    if (left == kUnit) {
-#pragma unroll
-        for (int k = 0; k < KMAX; ++k) {
-            if (k >= a.K) continue;
-            int p = par[k];
-            if (p < 0 || p >= a.K) p = k;
-            if (in_place && p == k) continue;
-            x[k] = load_as<uint4>(src + p * m.sk);
-        }
-#pragma unroll
-        for (int k = 0; k < KMAX; ++k) {
-            if (k >= a.K) continue;
-            int p = par[k];
-            if (p < 0 || p >= a.K) p = k;
-            if (in_place && p == k) continue;
-            __builtin_memcpy(dst + k * m.dk, &x[k], kUnit);
-        }
-    } else {
-        // the short last unit of a row, byte by byte
-        for (int j = 0; j < left; ++j) {
-            uint8_t y[KMAX];
-#pragma unroll
-            for (int k = 0; k < KMAX; ++k) {
-                if (k >= a.K) continue;
-                int p = par[k];
-                if (p < 0 || p >= a.K) p = k;
-                if (in_place && p == k) continue;
-                y[k] = (uint8_t)src[p * m.sk + j];
-            }
-#pragma unroll
-            for (int k = 0; k < KMAX; ++k) {
-                if (k >= a.K) continue;
-                int p = par[k];
-                if (p < 0 || p >= a.K) p = k;
-                if (in_place && p == k) continue;
-                dst[k * m.dk + j] = (char)y[k];
-            }
-        }
-    }
+    const uint32_t r = u / m.per_row, c = u % m.per_row;
+    const int64_t at = c < m.full ? (int64_t)c * kUnit : (int64_t)m.full * kUnit + (c - m.full);
+    const char *src = m.src + (int64_t)b * m.sb + (int64_t)r * m.sr + at;
+    char *dst = m.dst + (int64_t)b * m.db + (int64_t)r * m.dr + at;
+    if (c < m.full) move_unit<uint4, KMAX>(src, dst, m.sk, m.dk, from, K, in_place);
+    else move_unit<uint8_t, KMAX>(src, dst, m.sk, m.dk, from, K, in_place);
 }
 
 constexpr int kWalkThreads = 1024;
@@ -217,7 +200,7 @@ int launch_beam_reorder(const fa_beam_item *items, int n, int B, int K, const in
     // every item must fit before the first is launched
     for (int i = 0; i < n; ++i) {
         const fa_beam_item &x = items[i];
-        const int64_t per_row = x.row_bytes / kUnit + (x.row_bytes % kUnit != 0);
+        const int64_t per_row = x.row_bytes / kUnit + x.row_bytes % kUnit;
         if (x.rows == 0 || per_row == 0) continue;
         if (per_row > 0xffffffffLL || x.rows > 0xffffffffLL / per_row) return -1;
         const int64_t blocks = (x.rows * per_row + kMoveThreads - 1) / kMoveThreads;
@@ -242,8 +225,8 @@ int launch_beam_reorder(const fa_beam_item *items, int n, int B, int K, const in
             m.db = x.dst_batch_stride;
             m.dk = x.dst_beam_stride;
             m.dr = x.dst_row_stride;
-            m.row_bytes = x.row_bytes;
-            m.per_row = (uint32_t)((x.row_bytes + kUnit - 1) / kUnit);
+            m.full = (uint32_t)(x.row_bytes / kUnit);
+            m.per_row = (uint32_t)(m.full + x.row_bytes % kUnit);
             m.units = (uint32_t)(x.rows * m.per_row);
             m.blocks = (m.units + (uint64_t)kMoveThreads - 1) / kMoveThreads;
             m.first = (uint32_t)blocks;
