@@ -9,7 +9,6 @@ namespace {
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveItems = 24;  // items of one launch: their descriptors travel as kernel arguments
-constexpr int kUnit = 16;       // bytes a thread moves per slot
 
 struct MoveItem {
     const char *src;
@@ -28,33 +27,11 @@ struct MoveArgs {
 };
 static_assert(sizeof(MoveArgs) <= 4096, "kernel arguments");
 
-template <class U, int KMAX>
-__device__ __forceinline__ void move_unit(const char *src, char *dst, int64_t sk, int64_t dk,
-                                          const int (&from)[KMAX], int K, bool in_place)
-{
-    U x[KMAX];
-#pragma unroll
-    for (int k = 0; k < KMAX; ++k) {
-        if (k < K && !(in_place && from[k] == k)) {
-            U y;
-            __builtin_memcpy(&y, src + from[k] * sk, sizeof(U));  // any alignment
-            x[k] = y;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < KMAX; ++k) {
-        if (k < K && !(in_place && from[k] == k)) {
-            const U y = x[k];
-            __builtin_memcpy(dst + k * dk, &y, sizeof(U));
-        }
-    }
-}
-
-// One thread: one unit of every slot of a batch row, 16 bytes or one of the
-// row's last bytes.  All slots are loaded before any is stored, and no other
-// thread touches these bytes, so the permutation needs no second buffer
-// whatever the parents are.
-template <int KMAX>
+// One thread: N units of every slot of a batch row, each a U or one of the
+// row's last bytes.  All slots of a unit are loaded before any is stored, and
+// no other thread touches these bytes, so the permutation needs no second
+// buffer whatever the parents are.
+template <class U, int KMAX, int N>
 __global__ __launch_bounds__(kMoveThreads) void beam_move(MoveArgs a)
 {
     int i = 0;
@@ -62,8 +39,6 @@ __global__ __launch_bounds__(kMoveThreads) void beam_move(MoveArgs a)
     const MoveItem m = a.it[i];
     const uint32_t blk = blockIdx.x - m.first;
     const int b = blk / m.blocks, K = a.K;
-    const uint32_t u = (blk % m.blocks) * kMoveThreads + threadIdx.x;
-    if (u >= m.units) return;
     const int32_t *par = a.parents + (size_t)b * K;
     int from[KMAX];
 #pragma unroll
@@ -72,12 +47,55 @@ __global__ __launch_bounds__(kMoveThreads) void beam_move(MoveArgs a)
     for (int k = 0; k < KMAX; ++k)
         if (from[k] < 0 || from[k] >= K) from[k] = k;
     const bool in_place = m.src == m.dst;
-    const uint32_t r = u / m.per_row, c = u % m.per_row;
-    const int64_t at = c < m.full ? (int64_t)c * kUnit : (int64_t)m.full * kUnit + (c - m.full);
-    const char *src = m.src + (int64_t)b * m.sb + (int64_t)r * m.sr + at;
-    char *dst = m.dst + (int64_t)b * m.db + (int64_t)r * m.dr + at;
-    if (c < m.full) move_unit<uint4, KMAX>(src, dst, m.sk, m.dk, from, K, in_place);
-    else move_unit<uint8_t, KMAX>(src, dst, m.sk, m.dk, from, K, in_place);
+    const char *src[N];
+    char *dst[N];
+    int kind[N];  // 1 a unit, 2 a byte, 0 nothing
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint64_t u = ((uint64_t)(blk % m.blocks) * N + j) * kMoveThreads + threadIdx.x;
+        kind[j] = 0;
+        if (u < m.units) {
+            const uint32_t r = (uint32_t)u / m.per_row, c = (uint32_t)u % m.per_row;
+            const int64_t at = c < m.full ? (int64_t)c * sizeof(U)
+                                          : (int64_t)m.full * sizeof(U) + (c - m.full);
+            src[j] = m.src + (int64_t)b * m.sb + (int64_t)r * m.sr + at;
+            dst[j] = m.dst + (int64_t)b * m.db + (int64_t)r * m.dr + at;
+            kind[j] = c < m.full ? 1 : 2;
+        }
+    }
+    U x[N][KMAX];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (kind[j] == 1) {
+#pragma unroll
+            for (int k = 0; k < KMAX; ++k)
+                if (k < K && !(in_place && from[k] == k)) {
+                    U y;
+                    __builtin_memcpy(&y, src[j] + from[k] * m.sk, sizeof(U));  // any alignment
+                    x[j][k] = y;
+                }
+        }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (kind[j] == 1) {
+#pragma unroll
+            for (int k = 0; k < KMAX; ++k)
+                if (k < K && !(in_place && from[k] == k)) {
+                    const U y = x[j][k];
+                    __builtin_memcpy(dst[j] + k * m.dk, &y, sizeof(U));
+                }
+        }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (kind[j] == 2) {
+            uint8_t y[KMAX];
+#pragma unroll
+            for (int k = 0; k < KMAX; ++k)
+                if (k < K && !(in_place && from[k] == k)) y[k] = (uint8_t)src[j][from[k] * m.sk];
+#pragma unroll
+            for (int k = 0; k < KMAX; ++k)
+                if (k < K && !(in_place && from[k] == k)) dst[j][k * m.dk] = (char)y[k];
+        }
 }
 
 constexpr int kWalkThreads = 1024;
@@ -193,18 +211,20 @@ __global__ __launch_bounds__(kWalkThreads) void beam_walk(int T, int B, int K, W
 
 }  // namespace
 
-int launch_beam_reorder(const fa_beam_item *items, int n, int B, int K, const int32_t *parents,
-                        void *stream)
+namespace {
+
+template <class U, int KMAX, int N>
+int move_items(const fa_beam_item *items, int n, int B, int K, const int32_t *parents, hipStream_t st)
 {
-    hipStream_t st = (hipStream_t)stream;
+    constexpr int64_t kBlock = (int64_t)N * kMoveThreads;
+    const int64_t kUnit = sizeof(U);
     // every item must fit before the first is launched
     for (int i = 0; i < n; ++i) {
         const fa_beam_item &x = items[i];
         const int64_t per_row = x.row_bytes / kUnit + x.row_bytes % kUnit;
         if (x.rows == 0 || per_row == 0) continue;
         if (per_row > 0xffffffffLL || x.rows > 0xffffffffLL / per_row) return -1;
-        const int64_t blocks = (x.rows * per_row + kMoveThreads - 1) / kMoveThreads;
-        if (blocks * B > 0x7fffffffLL) return -1;
+        if ((x.rows * per_row + kBlock - 1) / kBlock * B > 0x7fffffffLL) return -1;
     }
     MoveArgs a;
     a.B = B;
@@ -228,22 +248,35 @@ int launch_beam_reorder(const fa_beam_item *items, int n, int B, int K, const in
             m.full = (uint32_t)(x.row_bytes / kUnit);
             m.per_row = (uint32_t)(m.full + x.row_bytes % kUnit);
             m.units = (uint32_t)(x.rows * m.per_row);
-            m.blocks = (m.units + (uint64_t)kMoveThreads - 1) / kMoveThreads;
+            m.blocks = (uint32_t)((m.units + kBlock - 1) / kBlock);
             m.first = (uint32_t)blocks;
             if (blocks + (int64_t)m.blocks * B > 0x7fffffffLL) break;
             blocks += (int64_t)m.blocks * B;
             ++a.n;
         }
         if (a.n == 0) continue;
-        const unsigned g = (unsigned)blocks;
-        if (K <= 4) beam_move<4><<<g, kMoveThreads, 0, st>>>(a);
-        else if (K <= 8) beam_move<8><<<g, kMoveThreads, 0, st>>>(a);
-        else if (K <= 16) beam_move<16><<<g, kMoveThreads, 0, st>>>(a);
-        else if (K <= 32) beam_move<32><<<g, kMoveThreads, 0, st>>>(a);
-        else beam_move<64><<<g, kMoveThreads, 0, st>>>(a);
+        beam_move<U, KMAX, N><<<(unsigned)blocks, kMoveThreads, 0, st>>>(a);
         if (hipError_t e = hipGetLastError(); e != hipSuccess) return (int)e;
     }
     return 0;
+}
+
+}  // namespace
+
+int launch_beam_reorder(const fa_beam_item *items, int n, int B, int K, const int32_t *parents,
+                        void *stream)
+{
+    hipStream_t st = (hipStream_t)stream;
+    // units of a thread: with one or two slots it needs a second unit to keep
+    // loads in flight (2 slots in place: 206 us with one, 145 with two; 4 slots:
+    // 268 and 282), with more the slots do.  Above 32 slots 16-byte units would
+    // leave a compute unit four wavefronts (64 slots: 670 us, with 8-byte ones 349).
+    if (K <= 2) return move_items<uint4, 2, 2>(items, n, B, K, parents, st);
+    if (K <= 4) return move_items<uint4, 4, 1>(items, n, B, K, parents, st);
+    if (K <= 8) return move_items<uint4, 8, 1>(items, n, B, K, parents, st);
+    if (K <= 16) return move_items<uint4, 16, 1>(items, n, B, K, parents, st);
+    if (K <= 32) return move_items<uint4, 32, 1>(items, n, B, K, parents, st);
+    return move_items<uint2, 64, 1>(items, n, B, K, parents, st);
 }
 
 int launch_beam_trace(int T, int B, int K, const int32_t *tokens, const int32_t *parents,
