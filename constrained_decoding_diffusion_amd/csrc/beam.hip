@@ -349,43 +349,6 @@ __device__ inline bool before(double k0, uint32_t i0, double k1, uint32_t i1)
     return k0 > k1 || (k0 == k1 && i0 < i1);
 }
 
-// The first K of the wavefront's R keys a lane (order: `before`; -inf is no
-// key), written in order to out_key / out_id; returns how many.
-template <int R, class Id>
-__device__ inline int wave_topk(double (&key)[R], Id id_of, int K, double *out_key,
-                                uint32_t *out_id, int lane)
-{
-    int n = 0;
-    while (n < K) {
-        double bk = -INFINITY;
-        uint32_t bi = ~0u;
-        int br = -1;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t id = id_of(r);
-            if (key[r] > -INFINITY && before(key[r], id, bk, bi)) {
-                bk = key[r];
-                bi = id;
-                br = r;
-            }
-        }
-        const double best = reduce_max_d(bk);
-        if (best == -INFINITY) break;
-        uint32_t low = bk == best ? bi : ~0u;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) low = min(low, (uint32_t)__shfl_xor((int)low, o));
-        if (bk == best && bi == low) {
-            out_key[n] = best;
-            out_id[n] = low;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r == br) key[r] = -INFINITY;
-        }
-        ++n;
-    }
-    return n;
-}
-
 // ascending as x ascends; 0 for -inf (no key)
 __device__ inline uint32_t ordered_key(double x)
 {
@@ -394,13 +357,25 @@ __device__ inline uint32_t ordered_key(double x)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// the largest multiple of 2^10 that at least n (<= 64) lanes' values reach
-__device__ inline uint32_t nth_largest(uint32_t x, int n)
+__device__ inline uint64_t ordered_key64(double x)
 {
-    uint32_t t = 0;
-    for (int bit = 31; bit >= 10; --bit)
-        if (__popcll(__ballot(x >= (t | (1u << bit)))) >= n) t |= 1u << bit;
-    return t;
+    if (!(x > -INFINITY)) return 0u;
+    const uint64_t u = (uint64_t)__double_as_longlong(x);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+// the largest multiples of 2^14 that at least n and n2 (<= 64) lanes' values reach
+__device__ inline void nth_largest(uint32_t x, int n, int n2, uint32_t *t, uint32_t *t2)
+{
+    uint32_t u = 0, w = 0;
+    for (int bit = 31; bit >= 14; --bit) {
+        const uint32_t cu = u | (1u << bit), cw = w | (1u << bit);
+        const int nu = __popcll(__ballot(x >= cu)), nw = __popcll(__ballot(x >= cw));
+        if (nu >= n) u = cu;
+        if (nw >= n2) w = cw;
+    }
+    *t = u;
+    *t2 = w;
 }
 
 struct PickShared {
@@ -408,11 +383,11 @@ struct PickShared {
     uint32_t id[kPickThreads];
     double sel_key[FA_BEAM_MAX];  // the first K of them, in order
     uint32_t sel_id[FA_BEAM_MAX];
-    int cnt[kPickWaves];
     uint32_t tau[2][kPickWaves];
     int rank[kPickThreads];
-    int n;  // candidates found, in either round
-    int n2;
+    int n, n2;     // candidates found, in either round
+    int count[3];  // of the narrowing's steps, in turn
+    int bad;
 };
 
 // The n candidates, unordered, in key / id: each ranked against all of them,
@@ -444,36 +419,8 @@ __device__ inline void rank_candidates(PickShared &sh, int n, int K)
     __syncthreads();
 }
 
-// Where more candidates tie than the list holds: the wavefronts' own first K
-// one by one, and the rank of each among all wavefronts'.
-template <int R, class Id>
-__device__ inline int rank_by_rounds(PickShared &sh, double (&key)[R], Id id_of, int K, int lane,
-                                     int wave)
-{
-    const int c = wave_topk(key, id_of, K, sh.key + wave * FA_BEAM_MAX, sh.id + wave * FA_BEAM_MAX, lane);
-    if (lane == 0) sh.cnt[wave] = c;
-    __syncthreads();
-    int total = 0;
-    for (int w = 0; w < kPickWaves; ++w) total += sh.cnt[w];
-    const int w0 = threadIdx.x / FA_BEAM_MAX, j0 = threadIdx.x % FA_BEAM_MAX;
-    if (j0 < sh.cnt[w0]) {
-        const double mk = sh.key[threadIdx.x];
-        const uint32_t mi = sh.id[threadIdx.x];
-        int rank = 0;
-        for (int w = 0; w < kPickWaves; ++w)
-            for (int j = 0; j < sh.cnt[w]; ++j)
-                rank += before(sh.key[w * FA_BEAM_MAX + j], sh.id[w * FA_BEAM_MAX + j], mk, mi);
-        if (rank < K) {
-            sh.sel_key[rank] = mk;
-            sh.sel_id[rank] = mi;
-        }
-    }
-    __syncthreads();
-    return min(total, K);
-}
-
-// appends the lanes' keys at or above the threshold to the candidate list;
-// counts all of them, also those past its end
+// appends the lanes' keys that are taken to the candidate list; counts all of
+// them, also those past its end
 template <int R, class Take, class Id>
 __device__ inline void append(PickShared &sh, int *count, const double (&key)[R], Take take, Id id_of,
                               int lane)
@@ -502,6 +449,48 @@ __device__ inline void append(PickShared &sh, int *count, const double (&key)[R]
     }
 }
 
+// Where more candidates tie than the list holds: the K first of all keys found
+// by bisection, on the key and then on the index, and only those listed.
+template <int R, class Id>
+__device__ inline void narrow(PickShared &sh, int *count, const double (&key)[R], Id id_of, int K,
+                              int lane)
+{
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid < 3) sh.count[tid] = 0;
+    if (tid == 0) *count = 0;
+    __syncthreads();
+    int step = 0;
+    // how many keys pass; the counter after next is cleared on the way
+    auto counted = [&](auto pass) {
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) c += __popcll(__ballot(pass(r)));
+        if (lane == 0) atomicAdd(&sh.count[step % 3], c);
+        if (tid == 0) sh.count[(step + 1) % 3] = 0;
+        __syncthreads();
+        return sh.count[step++ % 3];
+    };
+    uint64_t t = 0;  // the K-th largest key
+    for (int bit = 63; bit >= 0; --bit) {
+        const uint64_t c = t | (1ull << bit);
+        if (counted([&](int r) { return ordered_key64(key[r]) >= c; }) >= K) t = c;
+    }
+    const int above = counted([&](int r) { return ordered_key64(key[r]) > t; });
+    uint32_t last = 0;  // the most indices that leave fewer than K
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = last | (1u << bit);
+        if (above + counted([&](int r) { return ordered_key64(key[r]) == t && id_of(r) < c; }) <= K) last = c;
+    }
+    append(sh, count, key,
+           [&](int r) {
+               const uint64_t u = ordered_key64(key[r]);
+               return u > t || (u == t && id_of(r) < last);
+           },
+           id_of, lane);
+    __syncthreads();
+}
+
 __device__ inline void load8_as(int dtype, const void *row, int v, int V, float (&x)[8])
 {
     if (dtype == FA_F32) load8(static_cast<const float *>(row), v, V, x);
@@ -518,6 +507,10 @@ __device__ inline void load8_as(int dtype, const void *row, int v, int V, float 
 // threshold is the better of two that the wavefronts' lane maxima give: the
 // largest of their K-th largest, and the smallest of their ceil(K/16)-th
 // largest.  For the tokens it is the K-th granule maximum.
+//
+// What bounds it is latency: some eight dependent loads and as many barriers.
+// So everything that does not depend on an earlier answer is asked for first,
+// also where the answer may then not be used.
 template <int MODE, int RG, int RT>
 __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect a,
                                                           const float *__restrict__ gmax,
@@ -525,169 +518,183 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
                                                           const uint32_t *__restrict__ gmask,
                                                           int chunks)
 {
-    static_assert(kPickWaves * FA_BEAM_MAX == kPickThreads, "a thread per candidate slot");
+    static_assert(kPickWaves * FA_BEAM_MAX == kPickThreads, "a slot's wavefront");
+    constexpr double kLog2e = 1.4426950408889634;
     __shared__ double sh_lse[FA_BEAM_MAX];
     __shared__ double sh_score[FA_BEAM_MAX];
     __shared__ PickShared sh;
     __shared__ uint32_t sh_list[kPickWaves][kListWords];
-    __shared__ int sh_bad;
+    __shared__ uint32_t sh_new[kPickWaves][kWave];  // 64 words of a new state set
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int nG = beam_grans(d.V), W = (d.S + 31) / 32, Kin = a.Kin, K = a.K;
     const int row0 = b * Kin, M = Kin * nG;
     const bool flagged = a.status[b] != 0;
+    float gm[RG];
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+        const int i = r * kPickThreads + tid;
+        gm[r] = i < M ? gmax[(size_t)row0 * nG + i] : -INFINITY;
+    }
     sh.rank[tid] = 0;
     if (tid == 0) {
-        sh_bad = 0;
+        sh.bad = 0;
         sh.n = 0;
         sh.n2 = 0;
     }
-    int n = 0;
-    if (!flagged) {
-        float gm[RG];
+    __syncthreads();
+    for (int k = wave; k < Kin; k += kPickWaves) {
+        const float sc = a.scores_in[row0 + k];
+        double lse = MODE == FA_BEAM_LOGITS ? -INFINITY : 0.0;
+        bool bad = !(sc < INFINITY);
+        if (MODE == FA_BEAM_LOGITS) {
+            const double2 *pr = part + (size_t)(row0 + k) * nG;
+            const double2 none = make_double2(-INFINITY, 0.0);
+            const double2 p0 = lane < chunks ? pr[lane] : none;
+            const double2 p1 = lane + kWave < chunks ? pr[lane + kWave] : none;
+            if (sc > -INFINITY && !bad && !flagged) {
+                double m = fmax(p0.x, p1.x), s = 0.0;
+                bool odd = !(p0.x < INFINITY) || !(p1.x < INFINITY);
+                for (int c = lane + 2 * kWave; c < chunks; c += kWave) {
+                    m = fmax(m, pr[c].x);
+                    odd |= !(pr[c].x < INFINITY);
+                }
+                bad = __ballot(odd) != 0ull;
+                m = reduce_max_d(m);
+                if (!bad && m > -INFINITY) {
+                    auto term = [&](double2 p) {
+                        return p.y * exp2_poly(fmax((p.x - m) * kLog2e, -1100.0));
+                    };
+                    s = term(p0);
+                    if (chunks > kWave) s += term(p1);
+                    for (int c = lane + 2 * kWave; c < chunks; c += kWave) s += term(pr[c]);
+                    lse = m + log(reduce_sum_d(s));
+                }
+            }
+        }
+        if (lane == 0) {
+            sh_lse[k] = lse;
+            sh_score[k] = sc > -INFINITY && !flagged ? (double)sc : -INFINITY;
+            if (bad) atomicOr(&sh.bad, 1);
+        }
+    }
+    __syncthreads();
+    const uint32_t per_gran = nG > 1 ? 0xffffffffu / (uint32_t)nG + 1u : 0u;
+    auto beam_of = [&](uint32_t i) { return nG > 1 ? (int)__umulhi(i, per_gran) : (int)i; };
+    // x the value of a token or of a granule's best one
+    auto key_of = [&](double sc, double lse, float x) -> double {
+        if (!(x > -INFINITY) || !(sc > -INFINITY) || !(lse > -INFINITY)) return -INFINITY;
+        return MODE == FA_BEAM_PROBS ? sc + log((double)x) : sc + ((double)x - lse);
+    };
+    int ng;
+    {
+        double key[RG];
+        auto id_of = [&](int r) { return (uint32_t)(r * kPickThreads + tid); };
+        uint32_t top = 0;
+        bool bad = false;
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
-            const int i = r * kPickThreads + tid;
-            gm[r] = i < M ? gmax[(size_t)row0 * nG + i] : -INFINITY;
-        }
-        __syncthreads();
-        for (int k = wave; k < Kin; k += kPickWaves) {
-            const float sc = a.scores_in[row0 + k];
-            double lse = MODE == FA_BEAM_LOGITS ? -INFINITY : 0.0;
-            bool bad = !(sc < INFINITY);
-            if (MODE == FA_BEAM_LOGITS) {
-                // asked for before the score is known: an empty slot's are not used
-                const double2 *pr = part + (size_t)(row0 + k) * nG;
-                const double2 none = make_double2(-INFINITY, 0.0);
-                const double2 p0 = lane < chunks ? pr[lane] : none;
-                const double2 p1 = lane + kWave < chunks ? pr[lane + kWave] : none;
-                if (sc > -INFINITY && !bad) {
-                    double m = fmax(p0.x, p1.x), s = 0.0;
-                    bool odd = !(p0.x < INFINITY) || !(p1.x < INFINITY);
-                    for (int c = lane + 2 * kWave; c < chunks; c += kWave) {
-                        m = fmax(m, pr[c].x);
-                        odd |= !(pr[c].x < INFINITY);
-                    }
-                    bad = __ballot(odd) != 0ull;
-                    m = reduce_max_d(m);
-                    if (!bad && m > -INFINITY) {
-                        auto term = [&](double2 p) { return p.x > -INFINITY ? p.y * exp(p.x - m) : 0.0; };
-                        s = term(p0) + term(p1);
-                        for (int c = lane + 2 * kWave; c < chunks; c += kWave) s += term(pr[c]);
-                        lse = m + log(reduce_sum_d(s));
-                    }
+            key[r] = -INFINITY;
+            const uint32_t i = id_of(r);
+            if (i < (uint32_t)M) {
+                const int k = beam_of(i);
+                const double sc = sh_score[k];
+                // a maximum of a hypothesis that was not scanned is not there
+                if (sc > -INFINITY) {
+                    bad |= MODE == FA_BEAM_PROBS && gm[r] != gm[r];
+                    key[r] = key_of(sc, sh_lse[k], gm[r]);
                 }
             }
-            if (lane == 0) {
-                sh_lse[k] = lse;
-                sh_score[k] = sc > -INFINITY ? (double)sc : -INFINITY;
-                if (bad) atomicOr(&sh_bad, 1);
-            }
+            top = max(top, ordered_key(key[r]));
         }
-        __syncthreads();
-        const uint32_t per_gran = nG > 1 ? 0xffffffffu / (uint32_t)nG + 1u : 0u;
-        // x the value of a token or of a granule's best one
-        auto key_of = [&](int k, float x) -> double {
-            const double sc = sh_score[k], lse = sh_lse[k];
-            if (!(x > -INFINITY) || !(sc > -INFINITY) || !(lse > -INFINITY)) return -INFINITY;
-            return MODE == FA_BEAM_PROBS ? sc + log((double)x) : sc + ((double)x - lse);
-        };
-        int ng;
-        {
-            double key[RG];
-            auto id_of = [&](int r) { return (uint32_t)(r * kPickThreads + tid); };
-            uint32_t top = 0;
-            bool bad = false;
-#pragma unroll
-            for (int r = 0; r < RG; ++r) {
-                key[r] = -INFINITY;
-                const uint32_t i = id_of(r);
-                if (i < (uint32_t)M) {
-                    const int k = nG > 1 ? (int)__umulhi(i, per_gran) : (int)i;
-                    // a maximum of a hypothesis that was not scanned is not there
-                    if (sh_score[k] > -INFINITY) {
-                        bad |= MODE == FA_BEAM_PROBS && gm[r] != gm[r];
-                        key[r] = key_of(k, gm[r]);
-                    }
-                }
-                top = max(top, ordered_key(key[r]));
-            }
-            if (bad) atomicOr(&sh_bad, 1);
-            const uint32_t most = nth_largest(top, K);
-            const uint32_t some = nth_largest(top, (K + kPickWaves - 1) / kPickWaves);
+        if (bad) atomicOr(&sh.bad, 1);
+        uint32_t tau = 1;
+        if (M > 4 * kWave) {  // fewer are all ranked sooner than thinned out
+            uint32_t most, some;
+            nth_largest(top, K, (K + kPickWaves - 1) / kPickWaves, &most, &some);
             if (lane == 0) {
                 sh.tau[0][wave] = most;
                 sh.tau[1][wave] = some;
             }
             __syncthreads();
             uint32_t hi = 0, lo = ~0u;
+#pragma unroll
             for (int w = 0; w < kPickWaves; ++w) {
                 hi = max(hi, sh.tau[0][w]);
                 lo = min(lo, sh.tau[1][w]);
             }
-            const uint32_t tau = max(max(hi, lo), 1u);
-            append(sh, &sh.n, key, [&](int r) { return ordered_key(key[r]) >= tau; }, id_of, lane);
-            __syncthreads();
-            ng = sh.n;
-            if (ng <= kPickThreads) {
-                rank_candidates(sh, ng, K);
-                ng = min(ng, K);
-            } else {
-                ng = rank_by_rounds(sh, key, id_of, K, lane, wave);
-            }
+            tau = max(max(hi, lo), 1u);
         }
-        // their tokens; none before the last of K granule maxima is lost
-        const double floor_key = ng == K ? sh.sel_key[K - 1] : -INFINITY;
-        {
-            double key[RT * 8];
-            uint32_t base[RT];
+        append(sh, &sh.n, key, [&](int r) { return ordered_key(key[r]) >= tau; }, id_of, lane);
+        __syncthreads();
+        ng = sh.n;
+        if (ng > kPickThreads) {
+            narrow(sh, &sh.n, key, id_of, K, lane);
+            ng = sh.n;
+        }
+        rank_candidates(sh, ng, K);
+        ng = min(ng, K);
+    }
+    // their tokens; none before the last of K granule maxima is lost
+    const double floor_key = ng == K ? sh.sel_key[K - 1] : -INFINITY;
+    int n;
+    {
+        double key[RT * 8];
+        uint32_t base[RT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int q = r * kPickWaves + wave;
-                base[r] = 0;
+        for (int r = 0; r < RT; ++r) {
+            const int q = r * kPickWaves + wave;
+            base[r] = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) key[r * 8 + j] = -INFINITY;
-                if (q < ng) {
-                    const uint32_t i = sh.sel_id[q];
-                    const int k = nG > 1 ? (int)__umulhi(i, per_gran) : (int)i;
-                    const int g = (int)i - k * nG, v0 = g * kBeamGran + lane * 8;
-                    const uint32_t ok = (gmask[((size_t)row0 * nG + i) * kMaskWords + lane / 4] >>
-                                         (8 * (lane & 3))) & 255u;
-                    const size_t at = (size_t)b * a.batch_stride + (size_t)k * a.beam_stride;
-                    float x[8];
-                    load8_as(a.dtype, static_cast<const char *>(a.logits) + at * (a.dtype == FA_F32 ? 4 : 2),
-                             min(v0, d.V), d.V, x);
-                    base[r] = (uint32_t)k * (uint32_t)d.V + (uint32_t)v0;
+            for (int j = 0; j < 8; ++j) key[r * 8 + j] = -INFINITY;
+            if (q < ng) {
+                const uint32_t i = sh.sel_id[q];
+                const int k = beam_of(i);
+                const int g = (int)i - k * nG, v0 = g * kBeamGran + lane * 8;
+                const uint32_t ok = (gmask[((size_t)row0 * nG + i) * kMaskWords + lane / 4] >>
+                                     (8 * (lane & 3))) & 255u;
+                const size_t at = (size_t)b * a.batch_stride + (size_t)k * a.beam_stride;
+                float x[8];
+                load8_as(a.dtype, static_cast<const char *>(a.logits) + at * (a.dtype == FA_F32 ? 4 : 2),
+                         min(v0, d.V), d.V, x);
+                base[r] = (uint32_t)k * (uint32_t)d.V + (uint32_t)v0;
+                const double sc = sh_score[k], lse = sh_lse[k];
+                // logarithms of the few values that can reach the threshold alone
+                // (less what the rounding of the keys may hide)
+                const double slack = 1e-9 + 1e-15 * (fabs(floor_key) + fabs(sc));
+                const double least =
+                    MODE == FA_BEAM_PROBS && floor_key > -INFINITY
+                        ? exp2_poly(fmin(fmax((floor_key - sc - slack) * kLog2e, -1100.0), 1000.0))
+                        : 0.0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const double kk = (ok >> j) & 1u ? key_of(k, x[j]) : -INFINITY;
-                        if (kk >= floor_key) key[r * 8 + j] = kk;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    bool may = (ok >> j) & 1u;
+                    if (MODE == FA_BEAM_PROBS) may = may && (double)x[j] >= least && x[j] > 0.f;
+                    if (!__ballot(may)) continue;
+                    const double kk = may ? key_of(sc, lse, x[j]) : -INFINITY;
+                    if (kk >= floor_key) key[r * 8 + j] = kk;
                 }
             }
-            __syncthreads();  // sel_* is read
-            auto id_of = [&](int r) { return base[r / 8] + (uint32_t)(r % 8); };
-            append(sh, &sh.n2, key, [&](int r) { return key[r] > -INFINITY; }, id_of, lane);
-            __syncthreads();
+        }
+        __syncthreads();  // sel_* is read
+        auto id_of = [&](int r) { return base[r / 8] + (uint32_t)(r % 8); };
+        append(sh, &sh.n2, key, [&](int r) { return key[r] > -INFINITY; }, id_of, lane);
+        __syncthreads();
+        n = sh.n2;
+        if (n > kPickThreads) {
+            narrow(sh, &sh.n2, key, id_of, K, lane);
             n = sh.n2;
-            if (n <= kPickThreads) {
-                rank_candidates(sh, n, K);
-                n = min(n, K);
-            } else {
-                n = rank_by_rounds(sh, key, id_of, K, lane, wave);
-            }
         }
-        const bool bad = sh_bad != 0;
-        if (tid == 0) {
-            const int st = bad ? FA_ROW_BADPROB : (n == 0 ? FA_ROW_INFEASIBLE : 0);
-            if (st) a.status[b] = st;  // it was 0
-        }
-        if (bad) n = 0;
+        rank_candidates(sh, n, K);
+        n = min(n, K);
     }
-    // the slots: the states of each winner's token
+    if (sh.bad) n = 0;
+    if (tid == 0 && !flagged) {
+        const int st = sh.bad ? FA_ROW_BADPROB : (n == 0 ? FA_ROW_INFEASIBLE : 0);
+        if (st) a.status[b] = st;  // it was 0
+    }
+    // the slots: the states of each winner's token, 64 words of the set at a time
     for (int j = wave; j < K; j += kPickWaves) {
         const size_t o = (size_t)b * K + j;
-        uint32_t *to = a.states + o * W;
-        for (int w = lane; w < W; w += kWave) to[w] = 0u;
         const bool live = j < n;
         const int k = live ? (int)(sh.sel_id[j] / (uint32_t)d.V) : j % Kin;
         const int v = live ? (int)(sh.sel_id[j] % (uint32_t)d.V) : -1;
@@ -696,38 +703,44 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
             a.tokens[o] = v;
             a.parents[o] = k;
         }
-    }
-    __syncthreads();
-    for (int j = wave; j < n; j += kPickWaves) {
-        uint32_t *to = a.states + ((size_t)b * K + j) * W;
-        const int k = (int)(sh.sel_id[j] / (uint32_t)d.V), v = (int)(sh.sel_id[j] % (uint32_t)d.V);
-        each_states(set_of(a, row0 + k, W), W, sh_list[wave], lane, [&](int s, int m) {
-            auto add = [&](int t) {
-                if (!a.reach || has_bit(a.reach, t)) atomicOr(&to[t >> 5], 1u << (t & 31));
-            };
-            const bool mine = lane < m;
-            const int32_t *off = d.bm_off + (size_t)s * (nG + 1) + v / kBeamGran;
-            const int e0 = mine ? off[0] : 0, e1 = mine ? off[1] : 0;
-            const int d0 = mine ? d.bm_doff[s] : 0, d1 = mine ? d.bm_doff[s + 1] : 0;
-            const int s0 = mine ? d.bm_soff[s] : 0, s1 = mine ? d.bm_soff[s + 1] : 0;
-            each_item(e0, e1, m, lane, [&](int e) {
-                if (e < 0) return;
-                const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
-                if (en.x == v) add(en.y);
-            });
-            if (__ballot(d1 > d0))
-                each_item(d0, d1, m, lane, [&](int i) {
-                    if (i < 0) return;
-                    const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
-                    if (has_bit(d.dense_bits + (size_t)dn.x * d.dense_words, v)) add(dn.y);
+        for (int w0 = 0; w0 < W; w0 += kWave) {
+            uint32_t *bits = sh_new[wave];
+            bits[lane] = 0u;
+            wave_sync();
+            if (live)
+                each_states(set_of(a, row0 + k, W), W, sh_list[wave], lane, [&](int s, int m) {
+                    auto add = [&](int t) {
+                        const uint32_t w = (uint32_t)((t >> 5) - w0);
+                        if (w < (uint32_t)kWave && (!a.reach || has_bit(a.reach, t)))
+                            atomicOr(&bits[w], 1u << (t & 31));
+                    };
+                    const bool mine = lane < m;
+                    const int32_t *off = d.bm_off + (size_t)s * (nG + 1) + v / kBeamGran;
+                    const int e0 = mine ? off[0] : 0, e1 = mine ? off[1] : 0;
+                    const int d0 = mine ? d.bm_doff[s] : 0, d1 = mine ? d.bm_doff[s + 1] : 0;
+                    const int s0 = mine ? d.bm_soff[s] : 0, s1 = mine ? d.bm_soff[s + 1] : 0;
+                    each_item(e0, e1, m, lane, [&](int e) {
+                        if (e < 0) return;
+                        const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
+                        if (en.x == v) add(en.y);
+                    });
+                    if (__ballot(d1 > d0))
+                        each_item(d0, d1, m, lane, [&](int i) {
+                            if (i < 0) return;
+                            const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
+                            if (has_bit(d.dense_bits + (size_t)dn.x * d.dense_words, v)) add(dn.y);
+                        });
+                    if (__ballot(s1 > s0))
+                        each_item(s0, s1, m, lane, [&](int i) {
+                            if (i < 0) return;
+                            const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
+                            if (sg.x <= v && v < sg.y) add(sg.z);
+                        });
                 });
-            if (__ballot(s1 > s0))
-                each_item(s0, s1, m, lane, [&](int i) {
-                    if (i < 0) return;
-                    const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
-                    if (sg.x <= v && v < sg.y) add(sg.z);
-                });
-        });
+            wave_sync();
+            if (w0 + lane < W) a.states[o * W + w0 + lane] = bits[lane];
+            wave_sync();
+        }
     }
 }
 
@@ -818,6 +831,7 @@ template <int MODE, int RG>
 int pick_tokens(const DevTable &d, const BeamSelect &a, const ScanOut &o, int chunks, hipStream_t st)
 {
     if (a.K <= kPickWaves) return pick<MODE, RG, 1>(d, a, o, chunks, st);
+    if (a.K <= 2 * kPickWaves) return pick<MODE, RG, 2>(d, a, o, chunks, st);
     return pick<MODE, RG, FA_BEAM_MAX / kPickWaves>(d, a, o, chunks, st);
 }
 
@@ -837,6 +851,7 @@ int select(const DevTable &d, const BeamSelect &a, const ScanOut &o, hipStream_t
                                       : scan_any<Bf16, MODE>(d, a, o, NG, st);
     if (e) return e;
     if (a.Kin * nG <= 8 * kPickThreads) return pick_tokens<MODE, 8>(d, a, o, chunks, st);
+    if (a.Kin * nG <= 16 * kPickThreads) return pick_tokens<MODE, 16>(d, a, o, chunks, st);
     return pick_tokens<MODE, kBeamGranMax / kPickThreads>(d, a, o, chunks, st);
 }
 
