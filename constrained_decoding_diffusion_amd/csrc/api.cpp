@@ -382,7 +382,7 @@ namespace {
 int beam_size_check(const fa_table *t, int32_t B, int32_t Kin)
 {
     if (!t || B < 0 || Kin < 1 || Kin > FA_BEAM_MAX) return FA_EINVAL;
-    if ((int64_t)Kin * beam_grans(t->h.V) > kBeamGranMax) return FA_ETOOBIG;
+    if ((int64_t)Kin * beam_grans(t->h.V) > kBeamGranMax || B > kBeamRowsMax) return FA_ETOOBIG;
     return FA_OK;
 }
 
@@ -458,8 +458,7 @@ extern "C" int fa_beam_select(const fa_table *t, int32_t dtype, const void *logi
     a.parents = parents;
     a.states = states;
     a.status = row_status;
-    const int e = launch_beam_select(t->h.device_view(), a, (uint8_t *)ws, w, stream);
-    return e < 0 ? FA_ETOOBIG : hip_rc(e);
+    return hip_rc(launch_beam_select(t->h.device_view(), a, (uint8_t *)ws, w, stream));
 }
 
 extern "C" int fa_beam_reorder(const fa_beam_item *items, int32_t n_items, int32_t B, int32_t K,

@@ -244,13 +244,6 @@ __device__ inline const uint32_t *set_of(const BeamSelect &a, int row, int W)
     return a.states_in + (size_t)row * W;
 }
 
-template <class T>
-__device__ inline const T *row_of(const BeamSelect &a, int row)
-{
-    return static_cast<const T *>(a.logits) + (size_t)(row / a.Kin) * a.batch_stride +
-           (size_t)(row % a.Kin) * a.beam_stride;
-}
-
 // 2^t for t in about [-1100, 1], to 2e-12 relative: the integer part by the
 // exponent, 2^f on [-1/2, 1/2] by its degree-8 interpolation at the Chebyshev
 // points.  fp64 fused multiply-adds run at the fp32 rate on this chip, and the
@@ -314,17 +307,21 @@ template <class T, int MODE, int NG>
 __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamSelect a,
                                                                float *__restrict__ gmax,
                                                                double2 *__restrict__ part,
-                                                               uint32_t *__restrict__ gmask, int nblk)
+                                                               uint32_t *__restrict__ gmask)
 {
     __shared__ uint32_t sh_mask[kScanWaves][NG * kMaskWords + kListWords];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = blockIdx.x / nblk;
-    const int chunk = (blockIdx.x % nblk) * kScanWaves + wave;
+    // whatever is one for the wavefront is kept in scalar registers
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int b = blockIdx.z, k = blockIdx.y, row = b * a.Kin + k;
+    const int chunk = blockIdx.x * kScanWaves + wave;
     const int nG = beam_grans(d.V), W = (d.S + 31) / 32;
     const int g0 = chunk * NG;
     if (g0 >= nG) return;
-    if (a.status[row / a.Kin] != 0 || a.scores_in[row] == -INFINITY) return;
-    const T *x = row_of<T>(a, row);
+    if (a.status[b] != 0 || a.scores_in[row] == -INFINITY) return;
+    const T *x = static_cast<const T *>(a.logits) + (size_t)b * a.batch_stride + (size_t)k * a.beam_stride;
+    gmax += (size_t)row * nG + g0;
+    gmask += ((size_t)row * nG + g0) * kMaskWords;
+    part += (size_t)row * nG + chunk;
     float v[NG][8];
 #pragma unroll
     for (int i = 0; i < NG; ++i) load8(x, min((g0 + i) * kBeamGran + lane * 8, d.V), d.V, v[i]);
@@ -350,9 +347,9 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
             if (MODE == FA_BEAM_PROBS && __ballot(bad)) best = NAN;
             // for the second kernel, should the granule be among the best
             if (best > -INFINITY && lane < kMaskWords)
-                gmask[((size_t)row * nG + g0 + i) * kMaskWords + lane] = mask[i * kMaskWords + lane];
+                gmask[i * kMaskWords + lane] = mask[i * kMaskWords + lane];
         }
-        if (lane == 0 && g0 + i < nG) gmax[(size_t)row * nG + g0 + i] = best;
+        if (lane == 0 && g0 + i < nG) gmax[i] = best;
         if (MODE == FA_BEAM_LOGITS) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = __builtin_elementwise_maximum(m, v[i][j]);  // a NaN stays
@@ -379,7 +376,7 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
             }
             s = reduce_sum_d(s);
         }
-        if (lane == 0) part[(size_t)row * nG + chunk] = make_double2(ref, s);
+        if (lane == 0) *part = make_double2(ref, s);
     }
 }
 
@@ -563,7 +560,8 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
     __shared__ PickShared sh;
     __shared__ uint32_t sh_list[kPickWaves][kListWords];
     __shared__ uint32_t sh_new[kPickWaves][kWave];  // 64 words of a new state set
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nG = beam_grans(d.V), W = (d.S + 31) / 32, Kin = a.Kin, K = a.K;
     const int row0 = b * Kin, M = Kin * nG;
     const bool flagged = a.status[b] != 0;
@@ -843,10 +841,8 @@ int scan(const DevTable &d, const BeamSelect &a, const ScanOut &o, hipStream_t s
 {
     const int64_t waves = (beam_grans(d.V) + NG - 1) / NG;
     const int64_t nblk = (waves + kScanWaves - 1) / kScanWaves;
-    const int64_t blocks = nblk * a.B * a.Kin;
-    if (blocks > 0x7fffffff) return -1;
-    beam_scan<T, MODE, NG><<<(unsigned)blocks, kScanWaves * kWave, 0, st>>>(d, a, o.gmax, o.part,
-                                                                            o.gmask, (int)nblk);
+    beam_scan<T, MODE, NG><<<dim3((unsigned)nblk, a.Kin, a.B), kScanWaves * kWave, 0, st>>>(
+        d, a, o.gmax, o.part, o.gmask);
     return (int)hipGetLastError();
 }
 

@@ -67,6 +67,7 @@ constexpr size_t map_range_lds(int ncut)
 // wavefront's lane holds eight of them
 constexpr int kBeamGran = 512;
 constexpr int kBeamGranMax = 32768;   // granules of a row's hypotheses the selection holds in registers
+constexpr int kBeamRowsMax = 65535;   // batch rows of a launch (a grid dimension)
 constexpr int kBeamStatesMax = 1 << 18;  // states whose two bitsets fit the lookahead's LDS
 constexpr int beam_grans(int V) { return (V + kBeamGran - 1) / kBeamGran; }
 
@@ -411,9 +412,9 @@ BeamWs beam_ws_layout(const HostTable &t, int32_t B, int32_t Kin);
 int launch_beam_lookahead(const DevTable &d, int L, uint32_t *sets, void *stream);
 int launch_beam_start(const DevTable &d, int B, int K, float *scores, uint32_t *states,
                       void *stream);
-// FA_ETOOBIG as a negative value when the grid does not fit
 int launch_beam_select(const DevTable &d, const BeamSelect &a, uint8_t *ws, const BeamWs &w,
                        void *stream);
+// -1 when an item's workgroups do not fit a grid
 int launch_beam_reorder(const fa_beam_item *items, int n, int B, int K, const int32_t *parents,
                         void *stream);
 int launch_beam_trace(int T, int B, int K, const int32_t *tokens, const int32_t *parents,

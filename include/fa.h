@@ -473,7 +473,7 @@ enum { FA_BEAM_LOGITS = 0, FA_BEAM_PROBS = 1 };
  * fa_beam_sizes - workspace bytes of fa_beam_select with batch B and Kin
  * hypotheses per row, and the words W of one state set.  Either output may be
  * NULL.  Errors: FA_EINVAL (B < 0, Kin outside 1..FA_BEAM_MAX), FA_ETOOBIG
- * (Kin ceil(V / 512) > 32768: 262,144 tokens at 64 hypotheses).
+ * (Kin ceil(V / 512) > 32768: 262,144 tokens at 64 hypotheses; B > 65535).
  */
 int fa_beam_sizes(const fa_table *t, int32_t B, int32_t Kin, size_t *ws_bytes, int32_t *words);
 
@@ -532,7 +532,7 @@ int fa_beam_start(const fa_table *t, int32_t B, int32_t K, float *scores, uint32
  *                   it, gets K slots without a hypothesis.
  * A captured call may be replayed; nothing depends on earlier contents of ws.
  * Errors: FA_EINVAL (also a table without FA_BEAMS), FA_ETOOBIG (as
- * fa_beam_sizes, or more than 2^31 - 1 workgroups), FA_ESTATE, FA_EHIP.
+ * fa_beam_sizes), FA_ESTATE, FA_EHIP.
  */
 int fa_beam_select(const fa_table *t, int32_t dtype, const void *logits, int64_t batch_stride,
                    int64_t beam_stride, int32_t B, int32_t Kin, int32_t K, int32_t mode,
