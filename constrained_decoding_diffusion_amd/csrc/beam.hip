@@ -144,14 +144,10 @@ __device__ inline void each_states(const uint32_t *set, int W, uint32_t *list, i
 // Items [lo, hi) of every lane's own, taken 64 at a time by all lanes:
 // fn(item), -1 where a lane has none left.
 template <class Fn>
-__device__ inline void each_item(int lo, int hi, int n, int lane, Fn fn)
+__device__ inline void each_item(int lo, int hi, int lane, Fn fn)
 {
     const int cnt = hi - lo;
-    if (n == 1) {  // one owner, as on a deterministic automaton
-        const int l0 = __builtin_amdgcn_readfirstlane(lo), h0 = __builtin_amdgcn_readfirstlane(hi);
-        for (int i = l0; i < h0; i += kWave) fn(i + lane < h0 ? i + lane : -1);
-        return;
-    }
+    if (!__ballot(cnt > 0)) return;
     const int upto = scan_sum_i(cnt);
     const int total = __builtin_amdgcn_readlane(upto, 63);
     for (int i0 = 0; i0 < total; i0 += kWave) {
@@ -160,7 +156,6 @@ __device__ inline void each_item(int lo, int hi, int n, int lane, Fn fn)
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1)
             if (__shfl(upto, own + o - 1) <= i) own += o;
-        own = min(own, kWave - 1);
         const int at = i - (__shfl(upto, own) - __shfl(cnt, own));
         const int first = __shfl(lo, own);
         fn(i < total ? first + at : -1);
@@ -169,73 +164,165 @@ __device__ inline void each_item(int lo, int hi, int n, int lane, Fn fn)
 
 constexpr int kListWords = kWave;
 
+// the only state of a set of up to 64 words, as on a deterministic automaton,
+// in a scalar register; -1 for other sets
+__device__ inline int only_state(const uint32_t *set, int W, int lane)
+{
+    if (W > kWave) return -1;
+    const uint32_t word = lane < W ? set[lane] : 0u;
+    const unsigned long long nz = __ballot(word != 0u);
+    if (__popcll(nz) != 1) return -1;
+    const int l = __ffsll(nz) - 1;
+    const uint32_t bits = __builtin_amdgcn_readlane(word, l);
+    return __popc(bits) == 1 ? l * 32 + __ffs(bits) - 1 : -1;
+}
+
+// Parts of the mask of tokens t0 .. t0 + 32 words: an entry, a dense label and
+// the ranges lo < hi of the lanes.
+__device__ inline void mask_entry(const DevTable &d, const uint32_t *reach, int e, int t0, uint32_t *mask)
+{
+    const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
+    if (!reach || has_bit(reach, en.y)) atomicOr(&mask[(en.x - t0) >> 5], 1u << (en.x & 31));
+}
+
+__device__ inline void mask_dense(const DevTable &d, int j, int t0, int words, uint32_t *mask, int lane)
+{
+    const uint32_t *bits = d.dense_bits + (size_t)j * d.dense_words;
+    for (int w = lane; w < words; w += kWave) {
+        const int gw = t0 / 32 + w;
+        if (gw < d.dense_words) atomicOr(&mask[w], bits[gw]);
+    }
+}
+
+__device__ inline void mask_ranges(int lo, int hi, int t0, int words, uint32_t *mask, int lane)
+{
+    lo = max(lo, t0);
+    hi = min(hi, t0 + 32 * words);
+    unsigned long long hit = __ballot(lo < hi);
+    while (hit) {
+        const int l = __ffsll(hit) - 1;
+        hit &= hit - 1;
+        const int a = __builtin_amdgcn_readlane(lo, l) - t0;
+        const int b = __builtin_amdgcn_readlane(hi, l) - t0;
+        for (int w = (a >> 5) + lane; w <= (b - 1) >> 5; w += kWave) {
+            const uint32_t from = a > 32 * w ? ~0u << (a - 32 * w) : ~0u;
+            const uint32_t upto = b < 32 * w + 32 ? ~(~0u << (b - 32 * w)) : ~0u;
+            atomicOr(&mask[w], from & upto);
+        }
+    }
+}
+
 // mask[0 .. ng*16): bit t set when token g0*512 + t may follow the state set.
 // mask and list are the wavefront's own LDS words.
 __device__ inline void allowed_mask(const DevTable &d, const uint32_t *set, int W,
                                     const uint32_t *reach, int g0, int ng, uint32_t *mask,
                                     uint32_t *list, int lane)
 {
-    const int words = ng * kMaskWords, t0 = g0 * kBeamGran, t1 = t0 + ng * kBeamGran;
-    const int nG = beam_grans(d.V);
+    const int words = ng * kMaskWords, t0 = g0 * kBeamGran;
+    const int nG = beam_grans(d.V), g1 = min(g0 + ng, nG);
+    const int only = only_state(set, W, lane);
     for (int w = lane; w < words; w += kWave) mask[w] = 0u;
     wave_sync();
+    if (only >= 0) {
+        const int32_t *off = d.bm_off + (size_t)only * (nG + 1);
+        const int e0 = off[g0], e1 = off[g1];
+        const int d0 = d.bm_doff[only], d1 = d.bm_doff[only + 1];
+        const int s0 = d.bm_soff[only], s1 = d.bm_soff[only + 1];
+        for (int e = e0 + lane; e < e1; e += kWave) mask_entry(d, reach, e, t0, mask);
+        for (int i = d0; i < d1; ++i)
+            if (!reach || has_bit(reach, d.bm_dense[2 * (size_t)i + 1]))
+                mask_dense(d, d.bm_dense[2 * (size_t)i], t0, words, mask, lane);
+        for (int i = s0; i < s1; i += kWave) {
+            int lo = 0, hi = 0;
+            if (i + lane < s1) {
+                const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i + lane];
+                if (!reach || has_bit(reach, sg.z)) lo = sg.x, hi = sg.y;
+            }
+            mask_ranges(lo, hi, t0, words, mask, lane);
+        }
+        wave_sync();
+        return;
+    }
     each_states(set, W, list, lane, [&](int s, int n) {
         const bool mine = lane < n;
         const int32_t *off = d.bm_off + (size_t)s * (nG + 1);
-        const int e0 = mine ? off[g0] : 0, e1 = mine ? off[min(g0 + ng, nG)] : 0;
+        const int e0 = mine ? off[g0] : 0, e1 = mine ? off[g1] : 0;
         const int d0 = mine ? d.bm_doff[s] : 0, d1 = mine ? d.bm_doff[s + 1] : 0;
         const int s0 = mine ? d.bm_soff[s] : 0, s1 = mine ? d.bm_soff[s + 1] : 0;
-        each_item(e0, e1, n, lane, [&](int e) {
-            if (e < 0) return;
-            const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
-            if (!reach || has_bit(reach, en.y)) atomicOr(&mask[(en.x - t0) >> 5], 1u << (en.x & 31));
+        each_item(e0, e1, lane, [&](int e) {
+            if (e >= 0) mask_entry(d, reach, e, t0, mask);
         });
-        if (__ballot(d1 > d0)) {
-            each_item(d0, d1, n, lane, [&](int i) {
-                int j = -1;
-                if (i >= 0) {
-                    const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
-                    if (!reach || has_bit(reach, dn.y)) j = dn.x;
-                }
-                unsigned long long hit = __ballot(j >= 0);
-                while (hit) {
-                    const int l = __ffsll(hit) - 1;
-                    hit &= hit - 1;
-                    const uint32_t *bits =
-                        d.dense_bits + (size_t)__builtin_amdgcn_readlane(j, l) * d.dense_words;
-                    for (int w = lane; w < words; w += kWave) {
-                        const int gw = t0 / 32 + w;
-                        if (gw < d.dense_words) atomicOr(&mask[w], bits[gw]);
-                    }
-                }
-            });
-        }
-        if (__ballot(s1 > s0)) {
-            // range labels: those that meet the tokens, one by one
-            each_item(s0, s1, n, lane, [&](int i) {
-                int lo = 0, hi = 0;
-                if (i >= 0) {
-                    const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
-                    if (!reach || has_bit(reach, sg.z)) {
-                        lo = max(sg.x, t0);
-                        hi = min(sg.y, t1);
-                    }
-                }
-                unsigned long long hit = __ballot(lo < hi);
-                while (hit) {
-                    const int l = __ffsll(hit) - 1;
-                    hit &= hit - 1;
-                    const int a = __builtin_amdgcn_readlane(lo, l) - t0;
-                    const int b = __builtin_amdgcn_readlane(hi, l) - t0;
-                    for (int w = (a >> 5) + lane; w <= (b - 1) >> 5; w += kWave) {
-                        const uint32_t from = a > 32 * w ? ~0u << (a - 32 * w) : ~0u;
-                        const uint32_t upto = b < 32 * w + 32 ? ~(~0u << (b - 32 * w)) : ~0u;
-                        atomicOr(&mask[w], from & upto);
-                    }
-                }
-            });
-        }
+        each_item(d0, d1, lane, [&](int i) {
+            int j = -1;
+            if (i >= 0) {
+                const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
+                if (!reach || has_bit(reach, dn.y)) j = dn.x;
+            }
+            unsigned long long hit = __ballot(j >= 0);
+            while (hit) {
+                const int l = __ffsll(hit) - 1;
+                hit &= hit - 1;
+                mask_dense(d, __builtin_amdgcn_readlane(j, l), t0, words, mask, lane);
+            }
+        });
+        each_item(s0, s1, lane, [&](int i) {
+            int lo = 0, hi = 0;
+            if (i >= 0) {
+                const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
+                if (!reach || has_bit(reach, sg.z)) lo = sg.x, hi = sg.y;
+            }
+            mask_ranges(lo, hi, t0, words, mask, lane);
+        });
     });
+    wave_sync();
+}
+
+// The targets of a state set's edges that hold token v (and lie in reach):
+// bits[0 .. 64) of the words w0 .. w0 + 63.
+__device__ inline void next_states(const DevTable &d, const uint32_t *set, int W,
+                                   const uint32_t *reach, int v, int w0, uint32_t *bits,
+                                   uint32_t *list, int lane)
+{
+    const int nG = beam_grans(d.V), g = v / kBeamGran;
+    const int only = only_state(set, W, lane);
+    bits[lane] = 0u;
+    wave_sync();
+    auto add = [&](int t) {
+        const uint32_t w = (uint32_t)((t >> 5) - w0);
+        if (w < (uint32_t)kWave && (!reach || has_bit(reach, t))) atomicOr(&bits[w], 1u << (t & 31));
+    };
+    auto entry = [&](int e) {
+        const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
+        if (en.x == v) add(en.y);
+    };
+    auto dense = [&](int i) {
+        const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
+        if (has_bit(d.dense_bits + (size_t)dn.x * d.dense_words, v)) add(dn.y);
+    };
+    auto range = [&](int i) {
+        const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
+        if (sg.x <= v && v < sg.y) add(sg.z);
+    };
+    if (only >= 0) {
+        const int32_t *off = d.bm_off + (size_t)only * (nG + 1) + g;
+        const int e0 = off[0], e1 = off[1];
+        const int d0 = d.bm_doff[only], d1 = d.bm_doff[only + 1];
+        const int s0 = d.bm_soff[only], s1 = d.bm_soff[only + 1];
+        for (int e = e0 + lane; e < e1; e += kWave) entry(e);
+        for (int i = d0 + lane; i < d1; i += kWave) dense(i);
+        for (int i = s0 + lane; i < s1; i += kWave) range(i);
+    } else {
+        each_states(set, W, list, lane, [&](int s, int m) {
+            const bool mine = lane < m;
+            const int32_t *off = d.bm_off + (size_t)s * (nG + 1) + g;
+            const int e0 = mine ? off[0] : 0, e1 = mine ? off[1] : 0;
+            const int d0 = mine ? d.bm_doff[s] : 0, d1 = mine ? d.bm_doff[s + 1] : 0;
+            const int s0 = mine ? d.bm_soff[s] : 0, s1 = mine ? d.bm_soff[s + 1] : 0;
+            each_item(e0, e1, lane, [&](int e) { if (e >= 0) entry(e); });
+            each_item(d0, d1, lane, [&](int i) { if (i >= 0) dense(i); });
+            each_item(s0, s1, lane, [&](int i) { if (i >= 0) range(i); });
+        });
+    }
     wave_sync();
 }
 
@@ -741,39 +828,12 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
         }
         for (int w0 = 0; w0 < W; w0 += kWave) {
             uint32_t *bits = sh_new[wave];
-            bits[lane] = 0u;
-            wave_sync();
-            if (live)
-                each_states(set_of(a, row0 + k, W), W, sh_list[wave], lane, [&](int s, int m) {
-                    auto add = [&](int t) {
-                        const uint32_t w = (uint32_t)((t >> 5) - w0);
-                        if (w < (uint32_t)kWave && (!a.reach || has_bit(a.reach, t)))
-                            atomicOr(&bits[w], 1u << (t & 31));
-                    };
-                    const bool mine = lane < m;
-                    const int32_t *off = d.bm_off + (size_t)s * (nG + 1) + v / kBeamGran;
-                    const int e0 = mine ? off[0] : 0, e1 = mine ? off[1] : 0;
-                    const int d0 = mine ? d.bm_doff[s] : 0, d1 = mine ? d.bm_doff[s + 1] : 0;
-                    const int s0 = mine ? d.bm_soff[s] : 0, s1 = mine ? d.bm_soff[s + 1] : 0;
-                    each_item(e0, e1, m, lane, [&](int e) {
-                        if (e < 0) return;
-                        const int2 en = reinterpret_cast<const int2 *>(d.bm_ent)[e];
-                        if (en.x == v) add(en.y);
-                    });
-                    if (__ballot(d1 > d0))
-                        each_item(d0, d1, m, lane, [&](int i) {
-                            if (i < 0) return;
-                            const int2 dn = reinterpret_cast<const int2 *>(d.bm_dense)[i];
-                            if (has_bit(d.dense_bits + (size_t)dn.x * d.dense_words, v)) add(dn.y);
-                        });
-                    if (__ballot(s1 > s0))
-                        each_item(s0, s1, m, lane, [&](int i) {
-                            if (i < 0) return;
-                            const int4 sg = reinterpret_cast<const int4 *>(d.bm_seg)[i];
-                            if (sg.x <= v && v < sg.y) add(sg.z);
-                        });
-                });
-            wave_sync();
+            if (live) {
+                next_states(d, set_of(a, row0 + k, W), W, a.reach, v, w0, bits, sh_list[wave], lane);
+            } else {
+                bits[lane] = 0u;
+                wave_sync();
+            }
             if (w0 + lane < W) a.states[o * W + w0 + lane] = bits[lane];
             wave_sync();
         }
