@@ -62,17 +62,32 @@ __device__ inline double lane_move_d(double old, double x)
     return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
-template <class Op>
-__device__ inline float reduce_f(float x, Op op)  // op(x, x) = x
+// ascending as x ascends; 0 for -inf and NaN
+__device__ inline uint32_t ordered_f(float x)
 {
-    auto mv = [](uint32_t y) { return __uint_as_float(y); };
-    x = op(x, mv(lane_move<0x111, 0xf>(__float_as_uint(x), __float_as_uint(x))));
-    x = op(x, mv(lane_move<0x112, 0xf>(__float_as_uint(x), __float_as_uint(x))));
-    x = op(x, mv(lane_move<0x114, 0xf>(__float_as_uint(x), __float_as_uint(x))));
-    x = op(x, mv(lane_move<0x118, 0xf>(__float_as_uint(x), __float_as_uint(x))));
-    x = op(x, mv(lane_move<0x142, 0xa>(__float_as_uint(x), __float_as_uint(x))));
-    x = op(x, mv(lane_move<0x143, 0xc>(__float_as_uint(x), __float_as_uint(x))));
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t o = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+    return x > -INFINITY ? o : 0u;
+}
+
+__device__ inline float unordered_f(uint32_t o)
+{
+    if (o == 0u) return -INFINITY;
+    return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+}
+
+// the largest of the lanes' values, NaN left out (one instruction a step: the
+// integer maximum takes the moved lane as an operand, the fp32 one does not)
+__device__ inline float reduce_max_f(float v)
+{
+    uint32_t x = ordered_f(v);
+    x = max(x, lane_move<0x111, 0xf>(0u, x));
+    x = max(x, lane_move<0x112, 0xf>(0u, x));
+    x = max(x, lane_move<0x114, 0xf>(0u, x));
+    x = max(x, lane_move<0x118, 0xf>(0u, x));
+    x = max(x, lane_move<0x142, 0xa>(0u, x));
+    x = max(x, lane_move<0x143, 0xc>(0u, x));
+    return unordered_f(__builtin_amdgcn_readlane(x, 63));
 }
 
 __device__ inline double last_lane_d(double x)
@@ -391,10 +406,10 @@ __device__ inline double add_exps(double s, const float (&x)[N], int R)
 // different hypotheses are compared with each other, and two of them may lie
 // closer than an fp32 sum over 150,000 tokens resolves.
 template <class T, int MODE, int NG>
-__global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamSelect a,
-                                                               float *__restrict__ gmax,
-                                                               double2 *__restrict__ part,
-                                                               uint32_t *__restrict__ gmask)
+__global__ __launch_bounds__(kScanWaves *kWave, 8) void beam_scan(DevTable d, BeamSelect a,
+                                                                  float *__restrict__ gmax,
+                                                                  double2 *__restrict__ part,
+                                                                  uint32_t *__restrict__ gmask)
 {
     __shared__ uint32_t sh_mask[kScanWaves][NG * kMaskWords + kListWords];
     // whatever is one for the wavefront is kept in scalar registers
@@ -429,7 +444,7 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
                 best = fmaxf(best, y);
                 if (MODE == FA_BEAM_PROBS) bad |= on && !(y >= 0.f && y < INFINITY);
             }
-            best = reduce_f(best, [](float p, float q) { return fmaxf(p, q); });
+            best = reduce_max_f(best);
             // a bad probability travels as a NaN maximum
             if (MODE == FA_BEAM_PROBS && __ballot(bad)) best = NAN;
             // for the second kernel, should the granule be among the best
@@ -443,23 +458,25 @@ __global__ __launch_bounds__(kScanWaves *kWave) void beam_scan(DevTable d, BeamS
         }
     }
     if (MODE == FA_BEAM_LOGITS) {
-        m = reduce_f(m, [](float p, float q) { return __builtin_elementwise_maximum(p, q); });
-        double s = m, ref = m;  // NaN or +inf: the row is flagged
-        if (m == -INFINITY) s = 0.0;
-        else if (m < INFINITY) {
-            s = 0.0;
+        const bool odd = __ballot(!(m < INFINITY)) != 0ull;  // NaN or +inf: the row is flagged
+        m = reduce_max_f(m);
+        double s = 0.0, ref = odd ? (double)NAN : (double)m;
+        if (!odd && m > -INFINITY) {
             if (fabsf(m) < kExpFast) {
                 const int R = __builtin_amdgcn_readfirstlane((int)__builtin_rint((double)m * kLog2e));
 #pragma unroll
                 for (int i = 0; i < NG; ++i) s = add_exps(s, v[i], R);
                 ref = (double)R / kLog2e;
             } else {
-#pragma unroll
-                for (int i = 0; i < NG; ++i)
+#pragma unroll 1
+                for (int i = 0; i < NG; ++i) {
+                    float y[8];
+                    load8(x, min((g0 + i) * kBeamGran + lane * 8, d.V), d.V, y);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         // the difference first: it is exact, whatever the size of the logits
-                        s += exp2_poly(fmax(((double)v[i][j] - (double)m) * kLog2e, -1100.0));
+                        s += exp2_poly(fmax(((double)y[j] - ref) * kLog2e, -1100.0));
+                }
             }
             s = reduce_sum_d(s);
         }
@@ -475,9 +492,7 @@ __device__ inline bool before(double k0, uint32_t i0, double k1, uint32_t i1)
 // ascending as x ascends; 0 for -inf (no key)
 __device__ inline uint32_t ordered_key(double x)
 {
-    if (!(x > -INFINITY)) return 0u;
-    const uint32_t u = __float_as_uint((float)x);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return x > -INFINITY ? max(ordered_f((float)x), 1u) : 0u;
 }
 
 __device__ inline uint64_t ordered_key64(double x)
