@@ -547,17 +547,24 @@ def beam_reorder(tensors, parents, out=None):
         raise ValueError("out must hold one tensor for each of tensors")
     items = (_BeamItem * max(len(tensors), 1))()
     dev = parents.device
-    last = layout = None
-    for i, (s, d) in enumerate(zip(tensors, dst)):
-        key = (s.shape, s.stride(), s.dtype, s.device, d.shape, d.stride(), d.dtype, d.device)
-        if key != last:  # tensors of one layout follow each other
-            if s.dim() < 2 or s.shape[:2] != (B, K) or s.shape != d.shape or s.dtype != d.dtype:
-                raise ValueError(f"expected [{B}, {K}, ...] tensors, and out of the same shapes "
-                                 "and types")
-            if s.device != dev or d.device != dev:
-                raise ValueError(f"every tensor must be on {dev}")
-            layout, last = _move_layout(s, d), key
-        _BEAM_ITEM.pack_into(items, i * _BEAM_ITEM.size, s.data_ptr(), d.data_ptr(), *layout)
+    layout = shape = stride = dtype = dstride = None
+    at = 0
+    for s, d in zip(tensors, dst):
+        # tensors of one layout follow each other
+        if (s.stride() != stride or s.shape != shape or s.dtype != dtype
+                or (d is not s and d.stride() != dstride)):
+            if s.dim() < 2 or s.shape[:2] != (B, K):
+                raise ValueError(f"expected [{B}, {K}, ...] tensors, got {tuple(s.shape)}")
+            layout = None
+        if d is not s and (d.shape != s.shape or d.dtype != s.dtype or d.device != dev):
+            raise ValueError(f"out must have the shapes and types of tensors, on {dev}")
+        if s.device != dev:
+            raise ValueError(f"every tensor must be on {dev}")
+        if layout is None:
+            shape, stride, dtype, dstride = s.shape, s.stride(), s.dtype, d.stride()
+            layout = _move_layout(s, d)
+        _BEAM_ITEM.pack_into(items, at, s.data_ptr(), d.data_ptr(), *layout)
+        at += _BEAM_ITEM.size
     _launch("fa_beam_reorder", dev, items, len(tensors), B, K, parents.data_ptr())
     return dst
 
