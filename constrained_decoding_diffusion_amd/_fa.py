@@ -7,6 +7,7 @@ for device memory and the current stream.  Importing works without a GPU
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import struct
 
@@ -489,32 +490,34 @@ def beam_select(table: Table, logits, beams: BeamBuffers, out: BeamBuffers = Non
     return out
 
 
-def _slot_rows(t):
-    """(rows, row stride, row bytes) of a slot of t [B, K, ...]: its inner
-    dimensions as equal pieces at equal distances."""
-    e = t.element_size()
-    dims = [(n, s * e) for n, s in zip(t.shape[2:], t.stride()[2:]) if n != 1]
+def _slot_rows(shape, stride, item):
+    """(rows, row stride, row bytes) of a slot of a tensor [B, K, ...] with
+    elements of ``item`` bytes: its inner dimensions as equal contiguous
+    pieces at equal distances."""
+    dims = [(n, s * item) for n, s in zip(shape[2:], stride[2:]) if n != 1]
     if any(n == 0 for n, _ in dims):
         return 0, 0, 0
-    row = e
+    row = item
     while dims and dims[-1][1] == row:
         row *= dims.pop()[0]
     if not dims:
         return 1, row, row
-    n, stride = dims.pop()
-    while dims and dims[-1][1] == n * stride:
+    n, dist = dims.pop()
+    while dims and dims[-1][1] == n * dist:
         n *= dims.pop()[0]
     if dims:
         raise ValueError("a slot must be equal contiguous pieces at equal distances "
-                         f"(shape {tuple(t.shape)}, strides {t.stride()})")
-    return n, stride, row
+                         f"(shape {tuple(shape)}, strides {tuple(stride)})")
+    return n, dist, row
 
 
-def _move_layout(s, d):
-    """The fields of a _BeamItem behind its pointers: strides of source and
-    destination, rows, row bytes, both slots cut into the same pieces."""
-    rows, sr, row = _slot_rows(s)
-    rows_d, dr, row_d = _slot_rows(d)
+@functools.lru_cache(maxsize=256)
+def _move_layout(shape, src, dst, item):
+    """The fields of a _BeamItem behind its pointers, for tensors of one shape
+    and the strides src and dst: strides in bytes, rows, row bytes, both slots
+    cut into the same pieces."""
+    rows, sr, row = _slot_rows(shape, src, item)
+    rows_d, dr, row_d = _slot_rows(shape, dst, item)
     if row != row_d and rows * row:
         # one of them is contiguous over more dimensions
         piece = min(row, row_d)
@@ -524,8 +527,7 @@ def _move_layout(s, d):
             rows_d, dr, row_d = row_d // piece, piece, piece
     if (rows, row) != (rows_d, row_d):
         raise ValueError("tensors and out cut their slots into different pieces")
-    e = s.element_size()
-    return (s.stride(0) * e, s.stride(1) * e, sr, d.stride(0) * e, d.stride(1) * e, dr, rows, row)
+    return (src[0] * item, src[1] * item, sr, dst[0] * item, dst[1] * item, dr, rows, row)
 
 
 def beam_reorder(tensors, parents, out=None):
@@ -562,7 +564,7 @@ def beam_reorder(tensors, parents, out=None):
             raise ValueError(f"every tensor must be on {dev}")
         if layout is None:
             shape, stride, dtype, dstride = s.shape, s.stride(), s.dtype, d.stride()
-            layout = _move_layout(s, d)
+            layout = _move_layout(shape, stride, dstride, s.element_size())
         _BEAM_ITEM.pack_into(items, at, s.data_ptr(), d.data_ptr(), *layout)
         at += _BEAM_ITEM.size
     _launch("fa_beam_reorder", dev, items, len(tensors), B, K, parents.data_ptr())

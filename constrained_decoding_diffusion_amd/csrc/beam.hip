@@ -981,6 +981,11 @@ BeamWs beam_ws_layout(const HostTable &t, int32_t B, int32_t Kin)
 int launch_beam_lookahead(const DevTable &d, int L, uint32_t *sets, void *stream)
 {
     const size_t lds = 2 * (size_t)((d.S + 31) / 32) * sizeof(uint32_t);
+    if (lds > 48 * 1024) {
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&beam_reach),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return (int)e;
+    }
     beam_reach<<<1, kReachThreads, lds, (hipStream_t)stream>>>(d, L, sets);
     return (int)hipGetLastError();
 }

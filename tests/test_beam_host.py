@@ -34,6 +34,7 @@ def test_sizes():
     assert L.fa_beam_sizes(tb.handle, 3, 5, C.byref(n), C.byref(w)) == 0
     assert w.value == 1 and n.value >= 3 * 5 * 2 * 4
     assert L.fa_beam_sizes(tb.handle, 0, 1, None, None) == 0
+    assert L.fa_beam_sizes(tb.handle, 65536, 1, None, None) == _fa.FA_ETOOBIG
     for B, K in ((-1, 4), (1, 0), (1, 65), (1, -3)):
         assert L.fa_beam_sizes(tb.handle, B, K, None, None) == _fa.FA_EINVAL
     assert L.fa_beam_sizes(None, 1, 1, None, None) == _fa.FA_EINVAL
@@ -76,6 +77,11 @@ def test_lookahead_and_start_refusals():
     assert L.fa_beam_lookahead(tb.handle, -1, ONE, None) == _fa.FA_EINVAL
     assert L.fa_beam_lookahead(tb.handle, 4, None, None) == _fa.FA_EINVAL
     assert L.fa_beam_lookahead(tb.handle, 1 << 24, ONE, None) == _fa.FA_ETOOBIG
+    # two bitsets of more states would not fit the lookahead's LDS
+    n = 262145
+    big = fa.Table(n, 1, 0, [n - 1], np.arange(n - 1), np.arange(1, n), np.arange(n), np.zeros(n - 1),
+                   fa.FA_DFA)
+    assert L.fa_beam_lookahead(big.handle, 1, ONE, None) == _fa.FA_ETOOBIG
     assert L.fa_beam_start(tb.handle, 1, 4, ONE, ONE, None) == _fa.FA_ESTATE
     for B, K, s, q in ((-1, 4, ONE, ONE), (1, 0, ONE, ONE), (1, 65, ONE, ONE), (1, 4, None, ONE),
                        (1, 4, ONE, None)):
@@ -159,6 +165,6 @@ def test_slot_rows(shape, view, want):
     t = view(torch.zeros(shape))
     if want is None:
         with pytest.raises(ValueError):
-            _fa._slot_rows(t)
+            _fa._slot_rows(t.shape, t.stride(), 4)
     else:
-        assert _fa._slot_rows(t) == want
+        assert _fa._slot_rows(t.shape, t.stride(), 4) == want

@@ -291,6 +291,74 @@ def test_select_large_vocabularies():
     check(aut, x, np.array([[-1.0, -1.5]]), [[{0}, {0}]], 5, what="a million tokens")
 
 
+def test_select_large_state_sets():
+    """Sets of more states than a wavefront has lanes, over several words."""
+    aut = _aut("nfa", 2500, 3001, 61)
+    x, scores, sets = _inputs(aut, 2, 4, "f32", 62, many=300)
+    sets[1][2] = set(range(2500))
+    sets[0][1] = set(range(64, 128))
+    check(aut, x, scores, sets, 9, steps=4, what="300 states")
+    aut = _aut("range-nfa", 200, 5000, 63)
+    x, scores, sets = _inputs(aut, 2, 3, "bf16", 64, many=100)
+    check(aut, x, scores, sets, 12, "logits", 0, what="100 states, ranges")
+
+
+def test_select_many_states():
+    """An automaton of 70,000 states: bitsets of 2188 words, sets in the last
+    of them, and a lookahead of that size."""
+    S, V = 70000, 40
+    r = np.random.default_rng(65)
+    src = np.repeat(np.arange(S), 2)
+    dst = np.stack([(np.arange(S) + 1) % S, r.integers(0, S, S)], 1).reshape(-1)
+    tok = np.stack([np.arange(S) % V, (np.arange(S) + 7) % V], 1).reshape(-1)
+    aut = A.Automaton(S, V, 0, np.array([5, 69999], np.int32), src.astype(np.int32),
+                      dst.astype(np.int32), np.arange(2 * S + 1), tok.astype(np.int32), dfa=True)
+    x, scores, _ = _inputs(aut, 2, 3, "f32", 66)
+    sets = [[{69999}, {31, 32, 69000}, {5}], [{65536}, {0}, {2047, 2048}]]
+    check(aut, x, scores, sets, 4, what="70000 states")
+    tb = _table(aut, trim=False)
+    got = fa.beam_lookahead(tb, 3).cpu().numpy()
+    want = A.accepting_reach_sets(aut, 3)
+    np.testing.assert_array_equal(
+        got, R.words_of([[set(np.flatnonzero(w).tolist())] for w in want], got.shape[1])[:, 0])
+
+
+@pytest.mark.parametrize("mode", ["logits", "probs"])
+def test_select_ties_across_many_granules(mode):
+    """More granules tie than the candidate list holds."""
+    V = 200_000
+    aut = A._pack(1, V, 0, [0], [(0, 0, [3, V])], ranges=True, name="constant row")
+    x = torch.full((1, 1, V), 0.5, dtype=torch.bfloat16, device="cuda").expand(2, 5, V)
+    scores = np.array([[-1.0] * 5, [-2.0, -1.0, -1.0, -3.0, -1.0]])
+    for K in (5, 40):
+        check(aut, x, scores, [[{0}] * 5] * 2, K, mode, what="constant row")
+
+
+def test_select_huge_logits():
+    """Values up to the types' limits, alone and mixed with ordinary ones."""
+    aut = _aut("universal", 1, 3000, 0)
+    for dtype, t in DT.items():
+        big = torch.finfo(t).max
+        x, scores, sets = _inputs(aut, 4, 2, dtype, 67)
+        sets = [[{0}, {0}]] * 4
+        x = x.clone()
+        x[0, 0, 7] = big
+        x[0, 1, 2999] = -big
+        x[1] = -big
+        x[1, 0, 600:] = -big / 2
+        x[2, 0] = big
+        x[2, 1] *= 1e4 if dtype == "f16" else 1e12
+        x[3, 0, :1024] = -big
+        x[3, 1] += 3e4 if dtype == "f16" else 1e6
+        check(aut, x, scores, sets, 5, what=f"huge {dtype}")
+
+
+def test_select_many_rows():
+    aut = _aut("dfa", 9, 40, 68)
+    x, scores, sets = _inputs(aut, 3000, 24, "f16", 69)
+    check(aut, x, scores, sets, 3, steps=2, what="3000 rows")
+
+
 def test_lookahead_and_start():
     for kind, S, V in (("dfa", 40, 200), ("nfa", 300, 500), ("range", 20, 90), ("json", 33, 4000)):
         aut = _aut(kind, S, V, 50)
@@ -319,6 +387,7 @@ REORDER = [
     # B, K, inner shape, view, dtype
     (1, 1, (5,), lambda t: t, torch.float32),
     (2, 3, (), lambda t: t, torch.int64),
+    (3, 2, (3, 700, 5), lambda t: t[:, :, :, 2:691], torch.bfloat16),
     (2, 4, (7,), lambda t: t, torch.bfloat16),
     (3, 5, (3, 33, 5), lambda t: t[:, :, :, :29], torch.uint8),
     (2, 8, (4, 40, 64), lambda t: t[:, :, :, :33], torch.bfloat16),
