@@ -433,11 +433,12 @@ def beam_start(table: Table, B: int, K: int, device="cuda"):
     return beams
 
 
-def _beam_dtype(t):
+@functools.lru_cache(maxsize=None)
+def _beam_dtype(dtype):
     import torch
-    code = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}.get(t.dtype)
+    code = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA_BF16}.get(dtype)
     if code is None:
-        raise ValueError(f"logits must be float32, float16 or bfloat16, not {t.dtype}")
+        raise ValueError(f"logits must be float32, float16 or bfloat16, not {dtype}")
     return code
 
 
@@ -455,7 +456,7 @@ def beam_select(table: Table, logits, beams: BeamBuffers, out: BeamBuffers = Non
     if logits.dim() != 3 or logits.shape != (beams.B, beams.K, table.info["V"]):
         raise ValueError(f"logits has shape {tuple(logits.shape)}, expected "
                          f"{(beams.B, beams.K, table.info['V'])}")
-    dtype = _beam_dtype(logits)
+    dtype = _beam_dtype(logits.dtype)
     B, Kin, V = logits.shape
     sb, sk, sv = logits.stride()
     if not logits.is_cuda or (V > 1 and sv != 1):

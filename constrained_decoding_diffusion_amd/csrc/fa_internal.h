@@ -167,8 +167,8 @@ struct DevTable {
     const int32_t *sel_lb;     // [V/256 + 2] first sel_tok index at or after token 256 t
     const int32_t *pair_colpos;  // [npairs] position of each pair in col_pairs
     int32_t n_tm;              // token-major LIST entries
-    // FA_BEAMS: the edges of every state, token-sorted.  LIST pairs as
-    // (token, target) entries with the first entry at or after every granule,
+    // FA_BEAMS: the edges of every state.  LIST pairs as (token, target)
+    // entries in token order, with the first entry at or after every granule;
     // DENSE pairs as (dense index, target), RANGE pairs as (lo, hi, target)
     const int32_t *bm_off;     // [S][beam_grans(V) + 1]
     const int32_t *bm_ent;     // pairs

@@ -396,41 +396,39 @@ static bool build_beams(HostTable &t)
 {
     const int32_t nG = beam_grans(t.V);
     if ((int64_t)t.S * (nG + 1) > std::numeric_limits<int32_t>::max()) return false;
-    t.bm_off.assign((size_t)t.S * (nG + 1), 0);
+    // token-list entries: the token-major ones dealt out to their source
+    // states, which leaves each state's in token order
+    std::vector<int32_t> fill(t.S + 1, 0);
+    for (int32_t a : t.tm_a) fill[a + 1]++;
+    for (int32_t a = 0; a < t.S; ++a) fill[a + 1] += fill[a];
+    const std::vector<int32_t> first = fill;
+    t.bm_ent.resize(2 * t.tm_a.size());
+    for (int32_t k = 0; k < t.nsel(); ++k)
+        for (int32_t e = t.tm_off[k]; e < t.tm_off[k + 1]; ++e) {
+            const size_t at = (size_t)fill[t.tm_a[e]]++;
+            t.bm_ent[2 * at] = t.sel_tok[k];
+            t.bm_ent[2 * at + 1] = t.tm_b[e];
+        }
+    t.bm_off.resize((size_t)t.S * (nG + 1));
+    for (int32_t a = 0; a < t.S; ++a) {
+        int32_t e = first[a];
+        for (int32_t g = 0; g <= nG; ++g) {
+            while (e < first[a + 1] && t.bm_ent[2 * (size_t)e] < (int64_t)g * kBeamGran) ++e;
+            t.bm_off[(size_t)a * (nG + 1) + g] = e;
+        }
+    }
+    // dense labels and ranges, in the order of the state's pairs
     t.bm_doff.assign(t.S + 1, 0);
     t.bm_soff.assign(t.S + 1, 0);
-    std::vector<std::pair<int32_t, int32_t>> ent;
-    std::vector<std::pair<std::pair<int32_t, int32_t>, int32_t>> seg;
     for (int32_t a = 0; a < t.S; ++a) {
-        ent.clear();
-        seg.clear();
         for (int32_t q = t.row_ptr[a]; q < t.row_ptr[a + 1]; ++q) {
             const int32_t b = t.pair_b[q];
             if (t.pair_cls[q] == kDense) {
                 t.bm_dense.push_back(t.pair_aux[q]);
                 t.bm_dense.push_back(b);
             }
-            for (int32_t k = t.list_off[q]; k < t.list_off[q + 1]; ++k) ent.emplace_back(t.list_tok[k], b);
             for (int32_t k = t.seg_off[q]; k < t.seg_off[q + 1]; ++k)
-                seg.push_back({{t.seg_lo[k], t.seg_hi[k]}, b});
-        }
-        std::sort(ent.begin(), ent.end());
-        std::sort(seg.begin(), seg.end());
-        size_t e = 0;
-        const size_t base = t.bm_ent.size() / 2;
-        for (int32_t g = 0; g <= nG; ++g) {
-            while (e < ent.size() && ent[e].first < (int64_t)g * kBeamGran) ++e;
-            t.bm_off[(size_t)a * (nG + 1) + g] = (int32_t)(base + e);
-        }
-        for (auto &x : ent) {
-            t.bm_ent.push_back(x.first);
-            t.bm_ent.push_back(x.second);
-        }
-        for (auto &x : seg) {
-            t.bm_seg.push_back(x.first.first);
-            t.bm_seg.push_back(x.first.second);
-            t.bm_seg.push_back(x.second);
-            t.bm_seg.push_back(0);
+                t.bm_seg.insert(t.bm_seg.end(), {t.seg_lo[k], t.seg_hi[k], b, 0});
         }
         t.bm_doff[a + 1] = (int32_t)(t.bm_dense.size() / 2);
         t.bm_soff[a + 1] = (int32_t)(t.bm_seg.size() / 4);
