@@ -102,13 +102,14 @@ constexpr int kWalkThreads = 1024;
 constexpr int kWalkBytes = 48 * 1024;  // parents of a window, one byte each, and as much for the walked slots
 constexpr int kWalkTile = 64 * 65;     // tokens of a tile, rows padded to an odd length
 constexpr int kWalkLoads = 5;          // tokens of a tile a thread fetches, at most
-constexpr int kGone = 255;             // behind a parent out of range
+constexpr int kWalkMaps = kWalkThreads + kWalkThreads / 2;  // runs x (K + 1) slots, at most (K 1: 512 runs)
 
 struct WalkShape {
     int window;  // steps of a window
     int segs;    // runs of steps a window is walked in
     int tile;    // steps of a tile
     int part;    // steps whose tokens a workgroup writes
+    int quads;   // parents read four at a time
 };
 
 inline __host__ __device__ int tile_pitch(int K) { return K | 1; }
@@ -118,74 +119,96 @@ inline __host__ __device__ int tile_pitch(int K) { return K | 1; }
 // The walk back is T dependent steps; what bounds it is the latency of one
 // (a load from memory where the parents are left there: 0.28 us each).  Here
 // the parents of a window lie in LDS, `segs` runs of it are walked at once from
-// every slot they may be entered at, the runs' maps are composed (one LDS read
-// a run), and the runs are walked again from the slots the hypotheses do enter
-// them at: 2 window / segs + segs dependent LDS reads.  The tokens then go
-// through LDS tiles, so that both their rows [K] and the output's rows [T] are
-// read and written in whole lines.  2048 steps of 64 rows of 16 hypotheses
-// (25 MB): 23 us, against 590 us for a thread a hypothesis.
+// every slot they may be entered at, the runs' maps are composed from the end
+// by doubling, and the runs are walked again from the slots the hypotheses do
+// enter them at: 2 window / segs + log2 segs dependent LDS reads.  Slot K
+// stands for "no hypothesis" and leads to itself, so a step is one read.  The
+// tokens then go through LDS tiles, so that both their rows [K] and the
+// output's rows [T] are read and written in whole lines.  2048 steps of 64
+// rows of 16 hypotheses (25 MB): 590 us for a thread a hypothesis, 23 us with
+// the runs composed one after the other, 19 us like this.
 __global__ __launch_bounds__(kWalkThreads) void beam_walk(int T, int B, int K, WalkShape ws,
                                                           const int32_t *__restrict__ tokens,
                                                           const int32_t *__restrict__ parents,
                                                           int32_t *__restrict__ out)
 {
-    extern __shared__ int32_t sh_tile[];  // [kWalkTile] | parents | slots
+    extern __shared__ int32_t sh_tile[];  // [kWalkTile] | parents | slots, both [window][K + 1] bytes
+    const int P = K + 1;
     uint8_t *par = reinterpret_cast<uint8_t *>(sh_tile + kWalkTile);
-    uint8_t *slot = par + (size_t)ws.window * K;
-    __shared__ uint8_t map[kWalkThreads], entry[kWalkThreads], carry[FA_BEAM_MAX];
+    uint8_t *slot = par + (size_t)ws.window * P;
+    __shared__ uint8_t map[2][kWalkMaps], carry[2][FA_BEAM_MAX];
     const int b = blockIdx.x, tid = threadIdx.x;
     const int o0 = blockIdx.y * ws.part, o1 = min(o0 + ws.part, T);  // the steps to write
     const int rows = kWalkThreads / K;  // steps all threads take at once, a slot each
     const int tr = tid / K, k = tid % K;
-    const bool works = tr < rows;
+    const bool works = tr < rows, walks = tr < ws.segs;
     const int pitch = tile_pitch(K);
-    if (tid < K) carry[tid] = (uint8_t)tid;
+    auto slot_of = [&](int32_t p) { return (uint32_t)(p >= 0 && p < K ? p : K); };
+    if (tid < K) carry[0][tid] = (uint8_t)tid;
+    if (tid < ws.segs) map[0][tid * P + K] = map[1][tid * P + K] = (uint8_t)K;
+    int turn = 0;  // the carry in use
     for (int t1 = T; t1 > o0; t1 -= ws.window) {
         const int t0 = max(o0, t1 - ws.window), n = t1 - t0;
         const int w = max(min(n, o1 - t0), 0);  // the window's steps to write: its first w
-        const size_t base = ((size_t)t0 * B + b) * K + k;
+        const size_t row0 = ((size_t)t0 * B + b) * K;
         int32_t next[kWalkLoads];
         auto fetch = [&](int from) {
 #pragma unroll
             for (int i = 0; i < kWalkLoads; ++i) {
                 const int t = from + tr + i * rows;
-                if (works && t < min(w, from + ws.tile)) next[i] = tokens[base + (size_t)t * B * K];
+                if (works && t < min(w, from + ws.tile)) next[i] = tokens[row0 + k + (size_t)t * B * K];
             }
         };
         fetch(0);
-        if (works) {
-#pragma unroll 16
-            for (int t = tr; t < n; t += rows) {
-                const int32_t p = parents[base + (size_t)t * B * K];
-                par[t * K + k] = (uint8_t)(p >= 0 && p < K ? p : kGone);
+        if (ws.quads) {
+            const int kq = K / 4, rq = kWalkThreads / kq, q = tid % kq;
+            const int4 *src = reinterpret_cast<const int4 *>(parents + row0) + q;
+            if (tid / kq < rq) {
+#pragma unroll 8
+                for (int t = tid / kq; t < n; t += rq) {
+                    const int4 p = src[(size_t)t * B * kq];
+                    uint8_t *to = par + t * P + 4 * q;
+                    to[0] = (uint8_t)slot_of(p.x);
+                    to[1] = (uint8_t)slot_of(p.y);
+                    to[2] = (uint8_t)slot_of(p.z);
+                    to[3] = (uint8_t)slot_of(p.w);
+                }
             }
+        } else if (works) {
+#pragma unroll 8
+            for (int t = tr; t < n; t += rows)
+                par[t * P + k] = (uint8_t)slot_of(parents[row0 + k + (size_t)t * B * K]);
         }
+        for (int t = tid; t < n; t += kWalkThreads) par[t * P + K] = (uint8_t)K;
         __syncthreads();
         const int run = (n + ws.segs - 1) / ws.segs;
         const int lo = tr * run, hi = min(lo + run, n);
-        const bool walks = tr < ws.segs;
         if (walks) {
             int j = k;
-            for (int t = hi - 1; t >= lo; --t) j = j == kGone ? kGone : par[t * K + j];
-            map[tid] = (uint8_t)j;
+            for (int t = hi - 1; t >= lo; --t) j = par[t * P + j];
+            map[0][tr * P + k] = (uint8_t)j;
         }
         __syncthreads();
-        if (tid < K) {
-            int j = carry[tid];
-            for (int s = ws.segs - 1; s >= 0; --s) {
-                entry[s * K + tid] = (uint8_t)j;
-                j = j == kGone ? kGone : map[s * K + j];
+        // map[.][s]: where the slots at the end of run s + span - 1 come from
+        int cur = 0;
+        for (int span = 1; span < ws.segs; span *= 2) {
+            if (walks) {
+                const int j = tr + span < ws.segs ? map[cur][(tr + span) * P + k] : k;
+                map[1 - cur][tr * P + k] = map[cur][tr * P + j];
             }
-            carry[tid] = (uint8_t)j;
+            cur = 1 - cur;
+            __syncthreads();
         }
-        __syncthreads();
+        if (tid < K) carry[1 - turn][tid] = map[cur][carry[turn][tid]];
         if (walks && lo < w) {
-            int j = entry[tid];
+            int j = carry[turn][k];
+            if (tr + 1 < ws.segs) j = map[cur][(tr + 1) * P + j];
             for (int t = hi - 1; t >= lo; --t) {
-                slot[t * K + k] = (uint8_t)j;
-                j = j == kGone ? kGone : par[t * K + j];
+                slot[t * P + k] = (uint8_t)j;
+                j = par[t * P + j];
             }
         }
+        turn = 1 - turn;
         for (int from = 0; from < w; from += ws.tile) {
             const int m = min(ws.tile, w - from);
 #pragma unroll
@@ -198,9 +221,8 @@ __global__ __launch_bounds__(kWalkThreads) void beam_walk(int T, int B, int K, W
             for (int i = tid; i < K * ws.tile; i += kWalkThreads) {
                 const int kk = i / ws.tile, t = i % ws.tile;
                 if (t < m) {
-                    const int j = slot[(from + t) * K + kk];
-                    out[((size_t)b * K + kk) * T + t0 + from + t] =
-                        j == kGone ? -1 : sh_tile[t * pitch + j];
+                    const int j = slot[(from + t) * P + kk];
+                    out[((size_t)b * K + kk) * T + t0 + from + t] = j == K ? -1 : sh_tile[t * pitch + j];
                 }
             }
             __syncthreads();
@@ -283,11 +305,13 @@ int launch_beam_trace(int T, int B, int K, const int32_t *tokens, const int32_t 
                       int32_t *out, void *stream)
 {
     WalkShape ws;
-    ws.window = std::min(T, kWalkBytes / K);
-    ws.segs = 1;
-    while (ws.segs < kWalkThreads / K && (int64_t)ws.segs * ws.segs < 2 * (int64_t)ws.window) ++ws.segs;
+    ws.window = std::min(T, kWalkBytes / (K + 1));
+    // a run's steps cost as much as a level of the composition, so as many
+    // runs as there are threads for, of eight steps at least
+    ws.segs = std::max(1, std::min({kWalkThreads / K, kWalkMaps / (K + 1), ws.window / 8}));
     ws.tile = kWalkTile / tile_pitch(K) & ~63;
-    const size_t lds = kWalkTile * sizeof(int32_t) + 2 * (size_t)ws.window * K;
+    ws.quads = K % 4 == 0 && ((uintptr_t)parents & 15) == 0;
+    const size_t lds = kWalkTile * sizeof(int32_t) + 2 * (size_t)ws.window * (K + 1);
     if (lds > 48 * 1024) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&beam_walk),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -295,7 +319,8 @@ int launch_beam_trace(int T, int B, int K, const int32_t *tokens, const int32_t 
     }
     // workgroups that share a batch row: each repeats the walk through the steps
     // behind its own, and saves on the tiles (64 rows of 2048 steps, us at 1 /
-    // 2 / 4 / 8: 42 / 29 / 23 / 31, the last more than the compute units)
+    // 2 / 4 / 8 with the serial composition: 42 / 29 / 23 / 31, the last more
+    // workgroups than compute units)
     const int parts = std::max(1, std::min({8, T / 512, 256 / B}));
     ws.part = (T + parts - 1) / parts;
     beam_walk<<<dim3(B, (T + ws.part - 1) / ws.part), kWalkThreads, lds, (hipStream_t)stream>>>(T, B, K, ws, tokens, parents, out);
