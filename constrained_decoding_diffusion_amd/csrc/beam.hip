@@ -369,7 +369,7 @@ __device__ inline double exp2_poly(double t)
 // Adds sum_j 2^(x_j log2 e - R) to s, fp64, each term to 6e-11 relative: the
 // rounding constant C (kRound - R) of the fused multiply-add splits off the
 // whole part n, whose bits are the sum's low word, and 2^f on [-1/2, 1/2] is its
-// degree-7 interpolation at the Chebyshev points.  15 operations a term, each at
+// degree-7 interpolation at the Chebyshev points.  14 operations a term, each at
 // the rate of an fp32 one on this chip.  Needs |x_j| < 2^30 or -inf; whatever
 // lies below 2^-1000 counts as that.
 constexpr double kLog2e = 1.4426950408889634;
@@ -405,6 +405,12 @@ __device__ inline double add_exps(double s, const float (&x)[N], int R)
 // The sum of exponentials is held in fp64 from the first term on: keys of
 // different hypotheses are compared with each other, and two of them may lie
 // closer than an fp32 sum over 150,000 tokens resolves.
+//
+// On many long rows the vector ALUs bound it, 84% of their issue slots taken:
+// 725 instructions for 2048 tokens, 448 of them the exponentials' (64 rows of 16
+// hypotheses, 151,936 bf16 logits: 130 us, 2.4 TB/s; fp32, half as many: 77 us,
+// 4.0 TB/s).  On few it is the latency of the set, offset, edge and lookahead
+// loads that follow each other: 5 us.
 template <class T, int MODE, int NG>
 __global__ __launch_bounds__(kScanWaves *kWave, 8) void beam_scan(DevTable d, BeamSelect a,
                                                                   float *__restrict__ gmax,
@@ -646,9 +652,10 @@ __device__ inline void load8_as(int dtype, const void *row, int v, int V, float 
 // largest of their K-th largest, and the smallest of their ceil(K/16)-th
 // largest.  For the tokens it is the K-th granule maximum.
 //
-// What bounds it is latency: some eight dependent loads and as many barriers.
-// So everything that does not depend on an earlier answer is asked for first,
-// also where the answer may then not be used.
+// What bounds it is latency: some eight dependent loads and as many barriers
+// (K 4: 8 us, K 16 over 4752 granules: 16 us).  So everything that does not
+// depend on an earlier answer is asked for first, also where the answer may
+// then not be used.
 template <int MODE, int RG, int RT>
 __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect a,
                                                           const float *__restrict__ gmax,
@@ -949,9 +956,9 @@ int select(const DevTable &d, const BeamSelect &a, const ScanOut &o, hipStream_t
 {
     const int nG = beam_grans(d.V);
     // granules of a wavefront: few where the wavefronts would not fill the
-    // chip (4096 granules, us at 1 / 2 / 4: 7.8 / 8.6 / 11.0; 9504: 11.1 /
-    // 9.4 / 11.5), more where each one's fixed work counts (304,128: 230 /
-    // 177 / 163; at 8, 184)
+    // chip (4096 granules, us at 1 / 2 / 4: 8.2 / 8.5 / 10.4; 19,008: 10.3 /
+    // 7.3 / 8.6), more where each one's fixed work counts (304,128: 181 / 145 /
+    // 129; eight would leave five wavefronts a SIMD: 148)
     const int64_t all = (int64_t)a.B * a.Kin * nG;
     const int NG = all <= 8192 ? 1 : all <= 32768 ? 2 : 4;
     const int chunks = (nG + NG - 1) / NG;
