@@ -132,14 +132,23 @@ __device__ inline int scan_sum_i(int v)  // inclusive
     return (int)x;
 }
 
+// word w of a set of S states: bits past the last state are none, whatever the
+// caller's buffer holds there
+__device__ inline uint32_t set_word(const uint32_t *set, int w, int S)
+{
+    if (32 * w >= S) return 0u;
+    const uint32_t x = set[w];
+    return 32 * w + 32 <= S ? x : x & ((1u << (S & 31)) - 1u);
+}
+
 // A state set's members, up to 64 at a time, one a lane: calls fn(state, n)
 // with lanes 0 .. n-1 holding a state each.  `list` is 64 LDS words of the
 // wavefront's own.
 template <class Fn>
-__device__ inline void each_states(const uint32_t *set, int W, uint32_t *list, int lane, Fn fn)
+__device__ inline void each_states(const uint32_t *set, int S, uint32_t *list, int lane, Fn fn)
 {
-    for (int w0 = 0; w0 < W; w0 += kWave) {
-        const uint32_t word = w0 + lane < W ? set[w0 + lane] : 0u;
+    for (int w0 = 0; 32 * w0 < S; w0 += kWave) {
+        const uint32_t word = set_word(set, w0 + lane, S);
         if (!__ballot(word != 0u)) continue;
         const int own = __popc(word), upto = scan_sum_i(own);
         const int total = __builtin_amdgcn_readlane(upto, 63);
@@ -181,10 +190,10 @@ constexpr int kListWords = kWave;
 
 // the only state of a set of up to 64 words, as on a deterministic automaton,
 // in a scalar register; -1 for other sets
-__device__ inline int only_state(const uint32_t *set, int W, int lane)
+__device__ inline int only_state(const uint32_t *set, int S, int lane)
 {
-    if (W > kWave) return -1;
-    const uint32_t word = lane < W ? set[lane] : 0u;
+    if (S > 32 * kWave) return -1;
+    const uint32_t word = set_word(set, lane, S);
     const unsigned long long nz = __ballot(word != 0u);
     if (__popcll(nz) != 1) return -1;
     const int l = __ffsll(nz) - 1;
@@ -229,13 +238,12 @@ __device__ inline void mask_ranges(int lo, int hi, int t0, int words, uint32_t *
 
 // mask[0 .. ng*16): bit t set when token g0*512 + t may follow the state set.
 // mask and list are the wavefront's own LDS words.
-__device__ inline void allowed_mask(const DevTable &d, const uint32_t *set, int W,
-                                    const uint32_t *reach, int g0, int ng, uint32_t *mask,
-                                    uint32_t *list, int lane)
+__device__ inline void allowed_mask(const DevTable &d, const uint32_t *set, const uint32_t *reach,
+                                    int g0, int ng, uint32_t *mask, uint32_t *list, int lane)
 {
     const int words = ng * kMaskWords, t0 = g0 * kBeamGran;
     const int nG = beam_grans(d.V), g1 = min(g0 + ng, nG);
-    const int only = only_state(set, W, lane);
+    const int only = only_state(set, d.S, lane);
     for (int w = lane; w < words; w += kWave) mask[w] = 0u;
     wave_sync();
     if (only >= 0) {
@@ -258,7 +266,7 @@ __device__ inline void allowed_mask(const DevTable &d, const uint32_t *set, int 
         wave_sync();
         return;
     }
-    each_states(set, W, list, lane, [&](int s, int n) {
+    each_states(set, d.S, list, lane, [&](int s, int n) {
         const bool mine = lane < n;
         const int32_t *off = d.bm_off + (size_t)s * (nG + 1);
         const int e0 = mine ? off[g0] : 0, e1 = mine ? off[g1] : 0;
@@ -294,12 +302,11 @@ __device__ inline void allowed_mask(const DevTable &d, const uint32_t *set, int 
 
 // The targets of a state set's edges that hold token v (and lie in reach):
 // bits[0 .. 64) of the words w0 .. w0 + 63.
-__device__ inline void next_states(const DevTable &d, const uint32_t *set, int W,
-                                   const uint32_t *reach, int v, int w0, uint32_t *bits,
-                                   uint32_t *list, int lane)
+__device__ inline void next_states(const DevTable &d, const uint32_t *set, const uint32_t *reach,
+                                   int v, int w0, uint32_t *bits, uint32_t *list, int lane)
 {
     const int nG = beam_grans(d.V), g = v / kBeamGran;
-    const int only = only_state(set, W, lane);
+    const int only = only_state(set, d.S, lane);
     bits[lane] = 0u;
     wave_sync();
     auto add = [&](int t) {
@@ -327,7 +334,7 @@ __device__ inline void next_states(const DevTable &d, const uint32_t *set, int W
         for (int i = d0 + lane; i < d1; i += kWave) dense(i);
         for (int i = s0 + lane; i < s1; i += kWave) range(i);
     } else {
-        each_states(set, W, list, lane, [&](int s, int m) {
+        each_states(set, d.S, list, lane, [&](int s, int m) {
             const bool mine = lane < m;
             const int32_t *off = d.bm_off + (size_t)s * (nG + 1) + g;
             const int e0 = mine ? off[0] : 0, e1 = mine ? off[1] : 0;
@@ -434,7 +441,7 @@ __global__ __launch_bounds__(kScanWaves *kWave, 8) void beam_scan(DevTable d, Be
 #pragma unroll
     for (int i = 0; i < NG; ++i) load8(x, min((g0 + i) * kBeamGran + lane * 8, d.V), d.V, v[i]);
     uint32_t *mask = sh_mask[wave];
-    allowed_mask(d, set_of(a, row, W), W, a.reach, g0, NG, mask, mask + NG * kMaskWords, lane);
+    allowed_mask(d, set_of(a, row, W), a.reach, g0, NG, mask, mask + NG * kMaskWords, lane);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
@@ -851,7 +858,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
         for (int w0 = 0; w0 < W; w0 += kWave) {
             uint32_t *bits = sh_new[wave];
             if (live) {
-                next_states(d, set_of(a, row0 + k, W), W, a.reach, v, w0, bits, sh_list[wave], lane);
+                next_states(d, set_of(a, row0 + k, W), a.reach, v, w0, bits, sh_list[wave], lane);
             } else {
                 bits[lane] = 0u;
                 wave_sync();

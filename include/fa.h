@@ -463,7 +463,8 @@ int fa_commit(int32_t B, int32_t L, int32_t V, const float *conf, const int32_t 
  *
  * State sets are bitsets over the table's compact states (fa_table_state_map
  * gives their original ids): bit s % 32 of word s / 32, W = ceil(S' / 32)
- * words.  On a DFA a live hypothesis has one bit set.
+ * words; bits past the last state are ignored.  On a DFA a live hypothesis has
+ * one bit set.
  */
 enum { FA_F32 = 0, FA_F16 = 1, FA_BF16 = 2 };
 enum { FA_BEAM_LOGITS = 0, FA_BEAM_PROBS = 1 };

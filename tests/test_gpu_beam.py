@@ -303,6 +303,16 @@ def test_select_large_state_sets():
     check(aut, x, scores, sets, 12, "logits", 0, what="100 states, ranges")
 
 
+@pytest.mark.parametrize("kind,S", [("dfa", 9), ("nfa", 70), ("nfa", 2100)])
+def test_select_ignores_bits_past_the_last_state(kind, S):
+    aut = _aut(kind, S, 700, 81)
+    x, scores, sets = _inputs(aut, 2, 3, "f32", 82, many=2 if kind == "nfa" else 1)
+    tb = _table(aut, trim=False)
+    beams = _beams(tb, scores, sets)
+    beams.states[..., -1] |= -1 << (S % 32)
+    check(aut, x, scores, sets, 5, what="bits past the last state", tb=tb, beams=beams)
+
+
 def test_select_many_states():
     """An automaton of 70,000 states: bitsets of 2188 words, sets in the last
     of them, and a lookahead of that size."""
