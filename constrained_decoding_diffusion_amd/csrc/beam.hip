@@ -570,17 +570,18 @@ __device__ inline void rank_candidates(PickShared &sh, int n, int K)
     __syncthreads();
 }
 
-// appends the lanes' keys that are taken to the candidate list; counts all of
-// them, also those past its end
+// appends the lanes' keys that are taken (of the first `used` of each) to the
+// candidate list; counts all of them, also those past its end
 template <int R, class Take, class Id>
-__device__ inline void append(PickShared &sh, int *count, const double (&key)[R], Take take, Id id_of,
-                              int lane)
+__device__ inline void append(PickShared &sh, int *count, const double (&key)[R], int used, Take take,
+                              Id id_of, int lane)
 {
     unsigned long long hit[R];
     int c = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        hit[r] = __ballot(take(r));
+        hit[r] = 0ull;
+        if (r < used) hit[r] = __ballot(take(r));
         c += __popcll(hit[r]);
     }
     if (c == 0) return;
@@ -633,7 +634,7 @@ __device__ inline void narrow(PickShared &sh, int *count, const double (&key)[R]
         const uint32_t c = last | (1u << bit);
         if (above + counted([&](int r) { return ordered_key64(key[r]) == t && id_of(r) < c; }) <= K) last = c;
     }
-    append(sh, count, key,
+    append(sh, count, key, R,
            [&](int r) {
                const uint64_t u = ordered_key64(key[r]);
                return u > t || (u == t && id_of(r) < last);
@@ -754,9 +755,9 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
                 if (sc > -INFINITY) {
                     bad |= MODE == FA_BEAM_PROBS && gm[r] != gm[r];
                     key[r] = key_of(sc, sh_lse[k], gm[r]);
+                    top = max(top, ordered_key(key[r]));
                 }
             }
-            top = max(top, ordered_key(key[r]));
         }
         if (bad) atomicOr(&sh.bad, 1);
         uint32_t tau = 1;
@@ -776,7 +777,8 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
             }
             tau = max(max(hi, lo), 1u);
         }
-        append(sh, &sh.n, key, [&](int r) { return ordered_key(key[r]) >= tau; }, id_of, lane);
+        append(sh, &sh.n, key, (M + kPickThreads - 1) / kPickThreads,
+               [&](int r) { return ordered_key(key[r]) >= tau; }, id_of, lane);
         __syncthreads();
         ng = sh.n;
         if (ng > kPickThreads) {
@@ -829,7 +831,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick(DevTable d, BeamSelect
         }
         __syncthreads();  // sel_* is read
         auto id_of = [&](int r) { return base[r / 8] + (uint32_t)(r % 8); };
-        append(sh, &sh.n2, key, [&](int r) { return key[r] > -INFINITY; }, id_of, lane);
+        append(sh, &sh.n2, key, RT * 8, [&](int r) { return key[r] > -INFINITY; }, id_of, lane);
         __syncthreads();
         n = sh.n2;
         if (n > kPickThreads) {
