@@ -456,6 +456,9 @@ def beam_select(table: Table, logits, beams: BeamBuffers, out: BeamBuffers = Non
     if logits.dim() != 3 or logits.shape != (beams.B, beams.K, table.info["V"]):
         raise ValueError(f"logits has shape {tuple(logits.shape)}, expected "
                          f"{(beams.B, beams.K, table.info['V'])}")
+    if beams.words != (table.info["S"] + 31) // 32:
+        raise ValueError(f"the beams hold state sets of {beams.words} words, the table's have "
+                         f"{(table.info['S'] + 31) // 32}")
     dtype = _beam_dtype(logits.dtype)
     B, Kin, V = logits.shape
     sb, sk, sv = logits.stride()

@@ -150,6 +150,15 @@ def test_binding_refuses_host_tensors_and_shapes():
         fa.beam_search(tb, None, 1, 0, 4)
 
 
+def test_binding_refuses_beams_of_another_table():
+    # the kernels read and write state sets as wide as the table's
+    tb, wide = _table(), _table(S=70, seed=3)
+    b = fa.BeamBuffers(tb, 2, 4, device="cpu")
+    assert wide.info["S"] > 32 and b.words == 1
+    with pytest.raises(ValueError, match="state sets"):
+        fa.beam_select(wide, torch.zeros(2, 4, 700), b)
+
+
 @pytest.mark.parametrize("shape,view,want", [
     ((2, 3, 5), lambda t: t, (1, 20, 20)),
     ((2, 3), lambda t: t, (1, 4, 4)),
