@@ -382,6 +382,8 @@ class BeamBuffers:
         _check("fa_beam_sizes", lib().fa_beam_sizes(table.handle, B, K, C.byref(n), C.byref(w)))
         self.B, self.K, self.words = B, K, w.value
         if like is not None:
+            if like.B != B:
+                raise ValueError(f"like has {like.B} rows, not {B}")
             device = like.scores.device
         self.scores = torch.empty((B, K), dtype=torch.float32, device=device)
         self.states = torch.empty((B, K, w.value), dtype=torch.int32, device=device)

@@ -159,6 +159,14 @@ def test_binding_refuses_beams_of_another_table():
         fa.beam_select(wide, torch.zeros(2, 4, 700), b)
 
 
+def test_buffers_share_status_within_one_batch_only():
+    tb = _table()
+    b = fa.BeamBuffers(tb, 2, 4, device="cpu")
+    assert fa.BeamBuffers(tb, 2, 9, like=b).status is b.status
+    with pytest.raises(ValueError):
+        fa.BeamBuffers(tb, 3, 4, like=b)
+
+
 @pytest.mark.parametrize("shape,view,want", [
     ((2, 3, 5), lambda t: t, (1, 20, 20)),
     ((2, 3), lambda t: t, (1, 4, 4)),
