@@ -543,7 +543,8 @@ def beam_reorder(tensors, parents, out=None):
     types, views included (the valid part of longer caches), each slot one
     contiguous piece or equal pieces at equal distances.  In place, or into
     ``out`` (tensors of the same shapes and types that share no memory with
-    the sources).  parents: cuda int32 [B, K].  Returns out, or tensors."""
+    the sources).  No destination may be there twice, nor share memory with
+    another tensor of the call.  parents: cuda int32 [B, K].  Returns out, or tensors."""
     import torch
     if parents.dim() != 2 or parents.dtype != torch.int32 or not parents.is_contiguous() \
             or not parents.is_cuda:

@@ -103,7 +103,7 @@ constexpr int kWalkThreads = 1024;
 constexpr int kWalkBytes = 48 * 1024;  // parents of a window, one byte each, and as much for the walked slots
 constexpr int kWalkTile = 64 * 65;     // tokens of a tile, rows padded to an odd length
 constexpr int kWalkLoads = 5;          // tokens of a tile a thread fetches, at most
-constexpr int kWalkMaps = kWalkThreads + kWalkThreads / 2;  // runs x (K + 1) slots, at most (K 1: 512 runs)
+constexpr int kWalkMaps = kWalkThreads + kWalkThreads / 2;  // runs x (K + 1) slots, at most (K 1: 768 runs)
 
 struct WalkShape {
     int window;  // steps of a window

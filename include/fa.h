@@ -550,12 +550,13 @@ int fa_beam_select(const fa_table *t, int32_t dtype, const void *logits, int64_t
  * the same strides) the item is reordered in place, whatever the parents
  * (repeated, crossing), and slots that keep their place are not touched;
  * otherwise the memory of src and dst must not overlap, and neither may the
- * slots of one dst.  A parent outside 0..K-1 counts as the slot's own index.
+ * slots of one dst, nor an item's dst and the memory of another item.  A
+ * parent outside 0..K-1 counts as the slot's own index.
  *   items    host array, read during the call; pointers are device pointers
  *   parents  device int32 [B][K], K in 1..FA_BEAM_MAX
  * Errors: FA_EINVAL (sizes, null pointers, negative strides, dst == src with
- * different strides), FA_ETOOBIG (2^32 or more 16-byte pieces in a slot, or
- * 2^31 or more workgroups), FA_EHIP.
+ * different strides, one dst twice), FA_ETOOBIG (2^32 or more 16-byte pieces
+ * in a slot, or 2^31 or more workgroups), FA_EHIP.
  */
 typedef struct fa_beam_item {
     const void *src;

@@ -117,6 +117,16 @@ def test_reorder_refusals():
     assert f(_item(row_bytes=0), 1, 2, 4, ONE, None) == 0
 
 
+def test_reorder_refuses_a_slot_moved_twice():
+    # two items with one destination: a slot moved in place would be read moved already
+    f = fa.lib().fa_beam_reorder
+    two = (_fa._BeamItem * 3)(_item()[0], _item(dst=1 << 21, rows=0)[0], _item(src=8192)[0])
+    assert f(two, 3, 2, 4, ONE, None) == _fa.FA_EINVAL
+    two[2].rows = 0          # an empty one moves nothing, and neither does the first then
+    two[0].row_bytes = 0
+    assert f(two, 3, 2, 4, ONE, None) == 0
+
+
 def test_trace_refusals():
     f = fa.lib().fa_beam_trace
     assert f(0, 2, 4, None, None, None, None) == 0
